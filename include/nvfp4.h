@@ -312,4 +312,8 @@ int32_t nvfp4_moe_grouped_gemm_lora(const nvfp4_moe_problem* p, const nvfp4_moe_
 }
 #endif
 
+/* The expert gate, and MXFP4 with its products (same library). */
+#include "nvfp4_gate.h"
+#include "nvfp4_mx.h"
+
 #endif /* NVFP4_H */

@@ -44,6 +44,23 @@ class MoeTensors(ctypes.Structure):
         "w2_codes", "w2_scales", "w2_global", "a13_scale", "a2_scale", "out")]
 
 
+class GateConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("top_k", ctypes.c_int64),
+                ("n_group", ctypes.c_int64), ("topk_group", ctypes.c_int64), ("group_top", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class MxMoeProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("top_k", ctypes.c_int64),
+                ("H", ctypes.c_int64), ("I", ctypes.c_int64)]
+
+
+class MxMoeTensors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "x", "topk_ids", "topk_weights", "w13_codes", "w13_scales", "w2_codes", "w2_scales", "out")]
+
+
 class MoeLora(ctypes.Structure):
     _fields_ = [("rank", ctypes.c_int64), ("scale", ctypes.c_float), ("a13", ctypes.c_void_p),
                 ("b13", ctypes.c_void_p), ("a2", ctypes.c_void_p), ("b2", ctypes.c_void_p)]
@@ -85,6 +102,17 @@ def lib() -> ctypes.CDLL:
             "nvfp4_moe_lora_workspace_size": (SZ, [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeLora)]),
             "nvfp4_moe_grouped_gemm_lora": (I32, [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeTensors),
                                                   ctypes.POINTER(MoeLora), P, SZ, P]),
+            "nvfp4_moe_gate": (I32, [ctypes.POINTER(GateConfig), P, P, P, P, P]),
+            "nvfp4_moe_gate_backward": (I32, [ctypes.POINTER(GateConfig), P, P, P, P, P]),
+            "nvfp4_mx_quantize": (I32, [P, I64, I64, P, P, P]),
+            "nvfp4_mx_quantize_columnwise": (I32, [P, I64, I64, P, P, P]),
+            "nvfp4_mx_dequantize": (I32, [P, P, I64, I64, P, P]),
+            "nvfp4_mx_gemm_workspace_size": (SZ, [I64, I64, I64]),
+            "nvfp4_mx_gemm": (I32, [P, I64, I64, I64, P, P, P, P, SZ, P]),
+            "nvfp4_mx_gemm_packed_workspace_size": (SZ, [I64, I64, I64]),
+            "nvfp4_mx_gemm_packed": (I32, [P, P, I64, I64, I64, P, P, P, P, SZ, P]),
+            "nvfp4_mx_moe_workspace_size": (SZ, [ctypes.POINTER(MxMoeProblem)]),
+            "nvfp4_mx_moe": (I32, [ctypes.POINTER(MxMoeProblem), ctypes.POINTER(MxMoeTensors), P, SZ, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -125,6 +153,21 @@ def _on(stream):
     else:
         with torch.cuda.stream(stream):
             yield
+
+
+@contextlib.contextmanager
+def _launch(device, stream):
+    """Run a wrapper body with `device` current and, when a stream is given,
+    that stream (which must be one of the device's), so that temporaries and
+    kernels share it; yields the stream's handle."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+    with contextlib.ExitStack() as stack:
+        if device.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            stack.enter_context(torch.cuda.stream(stream))
+        yield torch.cuda.current_stream().cuda_stream
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
@@ -435,3 +478,8 @@ def moe_grouped_gemm(x, topk_ids, topk_weights, w13_codes, w13_scales, w13_globa
             _check(lib().nvfp4_moe_grouped_gemm_lora(ctypes.byref(p), ctypes.byref(t), ctypes.byref(c), _ptr(ws),
                                                      ws.numel(), _stream(stream)), "nvfp4_moe_grouped_gemm_lora")
     return out
+
+
+from .gate import SCORE_SIGMOID, SCORE_SOFTMAX, moe_gate, moe_gate_backward  # noqa: E402
+from .mx import (mx_dequantize, mx_gemm, mx_gemm_packed, mx_gemm_packed_workspace_size,  # noqa: E402
+                 mx_gemm_workspace_size, mx_moe, mx_moe_workspace_size, mx_quantize, mx_quantize_columnwise)

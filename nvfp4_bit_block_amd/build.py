@@ -3,7 +3,7 @@
 Every translation unit is compiled for gfx950 only, with correctly rounded
 fp32 division and square root, fp32 denormals kept, and packed-fp32 VALU
 instructions disabled; the objects are linked into one shared library that
-exports the C ABI of ``include/nvfp4.h``.
+exports the C ABI of ``include/nvfp4.h`` and the two headers it includes.
 """
 from __future__ import annotations
 
@@ -20,7 +20,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libnvfp4.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["api.cpp", "quantize.hip", "transpose.hip", "gemv.hip", "gemm_a16.hip", "gemm_stream.hip", "moe.hip", "lora.hip"]
+SOURCES = ["api.cpp", "quantize.hip", "transpose.hip", "gemv.hip", "gemm_a16.hip", "gemm_stream.hip", "moe.hip", "lora.hip",
+           "mx_api.cpp", "gate.hip", "mx_quant.hip", "mx_gemm.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "mx_internal.hpp"
 #include "nvfp4.h"
 #include "nvfp4_internal.hpp"
 
@@ -426,6 +427,14 @@ T* at(void* base, size_t off) {
 }
 
 }  // namespace
+
+// The error text, for the entry points of mx_api.cpp (declared in
+// mx_internal.hpp).
+namespace nvfp4 {
+int32_t api_fail(int32_t status, const char* text) { return fail(status, "%s", text); }
+int32_t api_hip(hipError_t e, const char* where) { return hip_status(e, where); }
+void api_clear() { g_last_error[0] = '\0'; }
+}  // namespace nvfp4
 
 extern "C" {
 

@@ -1,0 +1,73 @@
+// mx_device.hpp -- MXFP4 on gfx950: E8M0 scales, the block encoder, and the
+// scaled matrix instructions.
+//
+// MXFP4 (OCP Microscaling Formats 1.0): E2M1 codes, one E8M0 byte s per 32
+// elements along a row, value q * 2^(s - 127).
+#pragma once
+
+#include "nvfp4_device.hpp"
+
+namespace nvfp4 {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// The byte's value as fp32, exact: 2^-127 is a subnormal pattern, 255 is NaN.
+__device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
+    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
+}
+
+// Scale byte of a block from its largest |x| as a bf16 magnitude pattern:
+// floor(log2 amax) - 2 is the exponent field less 2 + 127, clamped at 0 (a
+// subnormal's field is 0 and so clamps too, like zero); field 255 (an
+// infinity or a NaN in the block) stays 255.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax) {
+    const uint32_t f = amax >> 7;
+    return f == 255 ? 255u : f > 2 ? f - 2 : 0u;
+}
+
+// Eight bf16 (four words) -> eight codes under the scale value 2^(s - 127)
+// (its fp32 form; the conversion rounds to nearest even on the E2M1 grid,
+// saturates at 6 and keeps the sign, also of a zero; checked for every bf16
+// under every scale).
+__device__ __forceinline__ uint32_t mx_encode8(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float d) {
+    uint32_t o = 0;
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, w0), d, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, w1), d, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, w2), d, 2);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, w3), d, 3);
+    return o;
+}
+// fp32 -> bf16 pattern, round to nearest even; a NaN (a block of scale byte
+// 255 makes them) stays one.
+__device__ __forceinline__ uint32_t f32_to_bf16(float f) {
+    return f != f ? 0x7FC0u : f32_to_bf16_rne(f);
+}
+
+// The scale the encoder divides by: a block of byte 255 decodes as NaN
+// whatever its codes, so any finite value serves there.
+__device__ __forceinline__ float mx_divisor(uint32_t s) { return e8m0_to_f32(s == 255 ? 127u : s); }
+
+// Largest magnitude of a word's two bf16, as a pattern, folded into m.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t m, uint32_t w) {
+    return max(max(m, w & 0x7FFFu), (w >> 16) & 0x7FFFu);
+}
+
+// D += A B on the scaled matrix instructions.  32x32x64: lane l holds row
+// (column) l % 32 and the 32 K positions [32 (l / 32), + 32), one MX block,
+// as 16 code bytes; 16x16x128: row l % 16, block l / 16.  Byte SEL of the
+// lane's scale word is that block's E8M0 byte.  D: lane l holds column l % 32
+// (l % 16), rows 8 (r / 4) + 4 (l / 32) + r % 4 (4 (l / 16) + r).
+template <int SEL_A, int SEL_B>
+__device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
+    const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const i32x8 B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, SEL_A, (int)sa, SEL_B, (int)sb);
+}
+template <int SEL_A, int SEL_B>
+__device__ __forceinline__ f32x4 mx_mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+    const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const i32x8 B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, SEL_A, (int)sa, SEL_B, (int)sb);
+}
+
+}  // namespace nvfp4

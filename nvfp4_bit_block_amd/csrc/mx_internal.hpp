@@ -1,0 +1,69 @@
+// mx_internal.hpp -- launchers of the MXFP4 and gate kernels, shared between
+// the C ABI (mx_api.cpp) and the kernel translation units.
+#pragma once
+
+#include "nvfp4.h"
+#include "nvfp4_internal.hpp"
+
+namespace nvfp4 {
+
+// ------------------------------------------------------------ quantization --
+
+// Whether a tensor's flat pass (tile grid) fits one launch.
+bool mx_quantize_fits(int64_t rows, int64_t cols);
+bool mx_quantize_cols_fits(int64_t rows, int64_t cols);
+hipError_t launch_mx_quantize(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                              hipStream_t stream);
+hipError_t launch_mx_quantize_cols(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes_t, uint8_t* scales_t,
+                                   hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* y,
+                                hipStream_t stream);
+
+// ---------------------------------------------------------------- products --
+
+enum class MxEpi : int {
+    kStoreBf16 = 0,  // y = bf16(acc)
+    kGateUp = 1,     // h = bf16(silu(g) * u), stored as MXFP4
+    kDown = 2,       // Y = acc (fp32)
+};
+
+struct MxGemmArgs {
+    const uint8_t* a_codes = nullptr;   // activation [*, K/2] (gathered when a_rows is set)
+    const uint8_t* a_scales = nullptr;  // [*, K/32]
+    const int32_t* a_rows = nullptr;    // A row of output row r = a_rows[r] / a_div
+    int32_t a_div = 1;
+    int64_t a_src_rows = 0;             // rows of the source tensor (gathered operands)
+    const uint8_t* b_codes = nullptr;   // weights [N, K/2] per group
+    const uint8_t* b_scales = nullptr;
+    int64_t M = 0, N = 0, K = 0;
+    // grouping: rows of group e are [row_off[e], row_off[e+1]), its row tiles
+    // [tile_off[e], tile_off[e+1])
+    const int32_t* row_off = nullptr;
+    const int32_t* tile_off = nullptr;
+    int32_t groups = 0;
+    int32_t ntiles = 0;                 // set by the launcher
+    void* out = nullptr;                // kStoreBf16: bf16 [M, ldo]; kDown: fp32 [M, ldo]; kGateUp: codes [M, ldo/2]
+    uint8_t* out_scales = nullptr;      // kGateUp: [M, ldo/32]
+    int64_t ldo = 0;
+};
+
+// Row tile of the grouped launches.
+constexpr int kMxMoeBM = 128;
+// grid_m bounds the row tiles of a grouped launch (ungrouped: ignored).
+hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream);
+
+// -------------------------------------------------------------------- gate --
+
+hipError_t launch_gate(const nvfp4_gate_config& c, const void* logits, const float* bias, int32_t* ids,
+                       float* weights, hipStream_t stream);
+hipError_t launch_gate_backward(const nvfp4_gate_config& c, const void* logits, const int32_t* ids,
+                                const float* dweights, void* dlogits, hipStream_t stream);
+
+// ------------------------------------------------------------------ errors --
+
+// Sets the calling thread's error text and returns `status` (api.cpp).
+int32_t api_fail(int32_t status, const char* text);
+int32_t api_hip(hipError_t e, const char* where);
+void api_clear();
+
+}  // namespace nvfp4
