@@ -54,8 +54,26 @@ int32_t check_product(int64_t M, int64_t N, int64_t K) {
     return NVFP4_OK;
 }
 
+// Up to 64 activation rows run on the weight-streaming kernel, more on the
+// LDS tiles.
+bool streams(int64_t M) { return M <= kMxStreamMost; }
+// A bf16 activation that the streaming kernel quantizes itself.
+bool one_launch(int64_t M, int64_t K) { return streams(M) && mx_stream_quantizes(M, K); }
+
 hipError_t run_product(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int64_t N, int64_t K,
                        const uint8_t* w_codes, const uint8_t* w_scales, uint16_t* y, hipStream_t s) {
+    if (streams(M)) {
+        MxStreamArgs g;
+        g.a_codes = a_codes;
+        g.a_scales = a_scales;
+        g.b_codes = w_codes;
+        g.b_scales = w_scales;
+        g.M = M;
+        g.N = N;
+        g.K = K;
+        g.y = y;
+        return launch_mx_stream(g, s);
+    }
     MxGemmArgs g;
     g.a_codes = a_codes;
     g.a_scales = a_scales;
@@ -79,10 +97,29 @@ struct MxMoeLayout {
     size_t xc = 0, xs = 0, hc = 0, hs = 0, y = 0, total = 0;
 };
 
+// How the layer runs: slot by slot (no routing tables, two launches) while
+// few slots can meet on an expert, else sorted by expert, in row tiles of
+// about twice the mean rows of an expert: 16 or 32 on the streaming kernel,
+// kMxMoeBM on the LDS tiles.
+enum class MoePlan { kSlots, kStream16, kStream32, kTiles };
+MoePlan plan_mx_moe(const nvfp4_mx_moe_problem& p) {
+    const int64_t S = p.T * p.top_k;
+    if (S <= 64 && p.H <= ((int64_t)1 << 20)) return MoePlan::kSlots;
+    if (S <= 8 * p.E) return MoePlan::kStream16;
+    if (S <= 20 * p.E) return MoePlan::kStream32;
+    return MoePlan::kTiles;
+}
+
 MxMoeLayout layout_mx_moe(const nvfp4_mx_moe_problem& p) {
     MxMoeLayout l;
     const int64_t S = p.T * p.top_k;
     size_t off = 0;
+    if (plan_mx_moe(p) == MoePlan::kSlots) {
+        l.hc = off; off += packed_codes_bytes(S, p.I);
+        l.hs = off; off += packed_scales_bytes(S, p.I);
+        l.total = off;
+        return l;
+    }
     l.row_off = off; off += align_up((size_t)(p.E + 1) * 4);
     l.tile_off = off; off += align_up((size_t)(p.E + 1) * 4);
     l.perm = off; off += align_up((size_t)S * 4);
@@ -110,8 +147,10 @@ int32_t check_mx_moe(const nvfp4_mx_moe_problem* p) {
         p->I * p->H >= kBytes)
         return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_moe: an operand of 2 GiB or more");
     // workgroups of the grouped products (256 threads each, fewer than 2^32 in all)
+    // (the streaming forms: 512 threads, row tiles of 16, 32 columns of h or 16 of H)
     const int64_t mt = S / kMxMoeBM + p->E + 1, nt = std::max(p->I / 64, p->H / 128) + 1;
-    if (mt * nt >= ((int64_t)1 << 24)) return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_moe: too many tiles");
+    const int64_t ms = std::min(S, 20 * p->E) / 16 + p->E + 64, ns = std::max(p->I / 32, p->H / 16) + 1;
+    if (mt * nt >= ((int64_t)1 << 24) || ms * ns >= ((int64_t)1 << 23)) return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_moe: too many tiles");
     return NVFP4_OK;
 }
 
@@ -209,6 +248,7 @@ int32_t nvfp4_mx_gemm_packed(const uint8_t* a_codes, const uint8_t* a_scales, in
 
 size_t nvfp4_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || check_product(M, N, K) != NVFP4_OK) return 0;
+    if (one_launch(M, K)) return 0;
     return packed_codes_bytes(M, K) + packed_scales_bytes(M, K);
 }
 
@@ -226,6 +266,17 @@ int32_t nvfp4_mx_gemm(const uint16_t* x, int64_t M, int64_t N, int64_t K, const 
     if (need > 0 && (!workspace || workspace_bytes < need))
         return api_fail(NVFP4_ERR_WORKSPACE, "mx_gemm: workspace smaller than nvfp4_mx_gemm_workspace_size");
     hipStream_t s = as_stream(stream);
+    if (one_launch(M, K)) {
+        MxStreamArgs g;
+        g.x = x;
+        g.b_codes = w_codes;
+        g.b_scales = w_scales;
+        g.M = M;
+        g.N = N;
+        g.K = K;
+        g.y = y;
+        return api_hip(launch_mx_stream(g, s), "mx_gemm stream");
+    }
     uint8_t* const xc = at<uint8_t>(workspace, 0);
     uint8_t* const xs = at<uint8_t>(workspace, packed_codes_bytes(M, K));
     if (int32_t st = api_hip(launch_mx_quantize(x, M, K, xc, xs, s), "mx_gemm quantize")) return st;
@@ -259,6 +310,33 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
     hipStream_t s = as_stream(stream);
     const int64_t S = p->T * p->top_k;
     const int32_t E = (int32_t)p->E;
+    const MoePlan plan = plan_mx_moe(*p);
+    MxStreamArgs up, down;
+    up.b_codes = t->w13_codes;
+    up.b_scales = t->w13_scales;
+    up.M = S;
+    up.N = 2 * p->I;
+    up.K = p->H;
+    up.E = down.E = E;
+    up.top_k = down.top_k = (int32_t)p->top_k;
+    up.h_codes = at<uint8_t>(workspace, l.hc);
+    up.h_scales = at<uint8_t>(workspace, l.hs);
+    down.a_codes = up.h_codes;
+    down.a_scales = up.h_scales;
+    down.b_codes = t->w2_codes;
+    down.b_scales = t->w2_scales;
+    down.M = S;
+    down.N = p->H;
+    down.K = p->I;
+    if (plan == MoePlan::kSlots) {
+        up.x = t->x;
+        up.ids = down.ids = t->topk_ids;
+        down.slot_w = t->topk_weights;
+        down.y = t->out;
+        if (int32_t e = api_hip(launch_mx_slot_up(up, S, s), "mx_moe gate/up")) return e;
+        return api_hip(launch_mx_slot_down(down, p->T, s), "mx_moe down");
+    }
+    const int bm = plan == MoePlan::kStream16 ? 16 : plan == MoePlan::kStream32 ? 32 : kMxMoeBM;
     int32_t* row_off = at<int32_t>(workspace, l.row_off);
     int32_t* tile_off = at<int32_t>(workspace, l.tile_off);
     int32_t* perm = at<int32_t>(workspace, l.perm);
@@ -268,13 +346,27 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
     uint8_t* hc = at<uint8_t>(workspace, l.hc);
     uint8_t* hs = at<uint8_t>(workspace, l.hs);
     float* Y = at<float>(workspace, l.y);
-    int32_t st = api_hip(launch_moe_route(t->topk_ids, S, E, kMxMoeBM, row_off, tile_off, perm, inv,
+    int32_t st = api_hip(launch_moe_route(t->topk_ids, S, E, bm, row_off, tile_off, perm, inv,
                                           at<int32_t>(workspace, l.pos_group), at<int32_t>(workspace, l.route), s),
                          "mx_moe route");
     if (st) return st;
     st = api_hip(launch_mx_quantize(t->x, p->T, p->H, xc, xs, s), "mx_moe quantize");
     if (st) return st;
-    const int grid_m = (int)((S + kMxMoeBM - 1) / kMxMoeBM + E);
+    const int grid_m = (int)((S + bm - 1) / bm + std::min<int64_t>(E, S));
+    if (plan != MoePlan::kTiles) {
+        up.a_codes = xc;
+        up.a_scales = xs;
+        up.perm = perm;
+        up.row_off = down.row_off = row_off;
+        up.tile_off = down.tile_off = tile_off;
+        down.yf = Y;
+        st = api_hip(launch_mx_group_up(up, bm, grid_m, s), "mx_moe gate/up");
+        if (st) return st;
+        st = api_hip(launch_mx_group_down(down, bm, grid_m, s), "mx_moe down");
+        if (st) return st;
+        return api_hip(launch_moe_combine(Y, inv, t->topk_weights, p->T, (int32_t)p->top_k, p->H, t->out, s),
+                       "mx_moe combine");
+    }
     MxGemmArgs g1;
     g1.a_codes = xc;
     g1.a_scales = xs;

@@ -52,6 +52,38 @@ constexpr int kMxMoeBM = 128;
 // grid_m bounds the row tiles of a grouped launch (ungrouped: ignored).
 hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream);
 
+// Few activation rows (mx_stream.hip).
+struct MxStreamArgs {
+    const uint16_t* x = nullptr;        // bf16 activation, quantized by the kernel; or
+    const uint8_t* a_codes = nullptr;   // packed activation [*, K/2], [*, K/32]
+    const uint8_t* a_scales = nullptr;
+    const uint8_t* b_codes = nullptr;   // weights [E, N, K/2], [E, N, K/32] (plain: E = 1)
+    const uint8_t* b_scales = nullptr;
+    int64_t M = 0, N = 0, K = 0;
+    int32_t E = 1, top_k = 1;
+    const int32_t* ids = nullptr;       // slot forms: [T, top_k]
+    const float* slot_w = nullptr;      // kSlotDown: [T, top_k]
+    const int32_t* perm = nullptr;      // grouped forms: slot of each expert row,
+    const int32_t* row_off = nullptr;   // row and tile offsets as in MxGemmArgs
+    const int32_t* tile_off = nullptr;
+    uint16_t* y = nullptr;              // bf16 outputs
+    float* yf = nullptr;                // kGroupDown: fp32 [S, N]
+    uint8_t* h_codes = nullptr;         // gate/up forms: MXFP4 h [S, N/4], [S, N/64]
+    uint8_t* h_scales = nullptr;
+    int32_t ntiles = 0, slice = 0;      // set by the launcher
+};
+constexpr int kMxStreamMost = 64;       // activation rows of the plain form
+// Blocks of one row that a wave of the stream kernel quantizes at most, and
+// whether the plain form takes bf16 activations of this size.
+int mx_stream_slice(int64_t K);
+bool mx_stream_quantizes(int64_t M, int64_t K);
+hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream);
+hipError_t launch_mx_slot_up(const MxStreamArgs& g, int64_t slots, hipStream_t stream);
+hipError_t launch_mx_slot_down(const MxStreamArgs& g, int64_t tokens, hipStream_t stream);
+// bm (16 or 32): rows of one workgroup; mtiles bounds the row tiles.
+hipError_t launch_mx_group_up(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
+hipError_t launch_mx_group_down(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
+
 // -------------------------------------------------------------------- gate --
 
 hipError_t launch_gate(const nvfp4_gate_config& c, const void* logits, const float* bias, int32_t* ids,

@@ -3,7 +3,7 @@ routed-expert layers from router logits, and the gradient of those weights.
 Argument marshalling only, as in the package's ``__init__``."""
 from __future__ import annotations
 
-import ctypes
+import functools
 import math
 
 import torch
@@ -16,15 +16,21 @@ _SCORES = {SCORE_SOFTMAX: 0, SCORE_SIGMOID: 1}
 _LOGITS = (torch.float32, torch.bfloat16)
 
 
-def _config(logits, top_k, n_group, topk_group, group_top, score, renormalize, scale):
+@functools.lru_cache(maxsize=256)
+def _config(T, E, top_k, n_group, topk_group, group_top, score, renormalize, bf16, scale):
+    """The C struct of one problem (a pure function of its numbers)."""
     if score not in _SCORES:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
-    scale = float(scale)
     if not (math.isfinite(scale) and scale > 0.0):
         raise ValueError(f"scale must be finite and > 0, got {scale}")
-    T, E = logits.shape
     return nv.GateConfig(T, E, top_k, n_group, topk_group, group_top, _SCORES[score], 1 if renormalize else 0,
-                         0 if logits.dtype == torch.float32 else 1, scale)
+                         1 if bf16 else 0, scale)
+
+
+def _logits(logits):
+    nv._req(logits, "logits", _LOGITS, (None, None))
+    nv._cuda(logits, "logits")
+    return logits.shape[0], logits.shape[1], logits.device
 
 
 def moe_gate(logits, top_k, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1, group_top=1, renormalize=True,
@@ -36,37 +42,34 @@ def moe_gate(logits, top_k, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_grou
     gradient to it).  ``n_group`` runs of experts, of which the ``topk_group``
     with the largest sum of their ``group_top`` best choice values stay.  A
     row with fewer candidates than ``top_k`` ends in ids -1 of weight 0."""
-    nv._req(logits, "logits", _LOGITS, (None, None))
-    T, E = logits.shape
-    dev = nv._cuda(logits, "logits").device
+    T, E, dev = _logits(logits)
     if bias is not None:
-        nv._req(bias, "bias", nv._F32, (E,), dev)
-    c = _config(logits, top_k, n_group, topk_group, group_top, score, renormalize, scale)
-    with nv._launch(dev, stream) as s:
-        ids = nv._empty((T, top_k), torch.int32, dev) if ids is None else nv._req(ids, "ids", nv._I32, (T, top_k), dev)
-        weights = (nv._empty((T, top_k), torch.float32, dev) if weights is None else
-                   nv._req(weights, "weights", nv._F32, (T, top_k), dev))
-        nv._check(nv.lib().nvfp4_moe_gate(ctypes.byref(c), logits.data_ptr(),
-                                          None if bias is None else bias.data_ptr(), ids.data_ptr(),
-                                          weights.data_ptr(), s), "nvfp4_moe_gate")
-    return ids, weights
+        nv._arg(bias, "bias", nv._F32, (E,), dev)
+    c = _config(T, E, top_k, n_group, topk_group, group_top, score, bool(renormalize),
+                logits.dtype is torch.bfloat16, float(scale))
+
+    def body(s):
+        i = nv._out(ids, "ids", torch.int32, (T, top_k), dev)
+        w = nv._out(weights, "weights", torch.float32, (T, top_k), dev)
+        nv._check(nv.lib().nvfp4_moe_gate(c, logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                                          i.data_ptr(), w.data_ptr(), s), "nvfp4_moe_gate")
+        return i, w
+    return nv._launch(dev, stream, body)
 
 
 def moe_gate_backward(logits, ids, dweights, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, dlogits=None,
                       stream=None):
     """nvfp4_moe_gate_backward: the gradient of the forward call's weights with
     respect to its logits, [T, E] in their type, at the ids that it chose."""
-    nv._req(logits, "logits", _LOGITS, (None, None))
-    T, E = logits.shape
-    dev = nv._cuda(logits, "logits").device
+    T, E, dev = _logits(logits)
     nv._req(ids, "ids", nv._I32, (T, None), dev)
     top_k = ids.shape[1]
-    nv._req(dweights, "dweights", nv._F32, (T, top_k), dev)
-    c = _config(logits, top_k, 1, 1, 1, score, renormalize, scale)
-    with nv._launch(dev, stream) as s:
-        dlogits = (nv._empty((T, E), logits.dtype, dev) if dlogits is None else
-                   nv._req(dlogits, "dlogits", (logits.dtype,), (T, E), dev))
-        nv._check(nv.lib().nvfp4_moe_gate_backward(ctypes.byref(c), logits.data_ptr(), ids.data_ptr(),
-                                                   dweights.data_ptr(), dlogits.data_ptr(), s),
-                  "nvfp4_moe_gate_backward")
-    return dlogits
+    nv._arg(dweights, "dweights", nv._F32, (T, top_k), dev)
+    c = _config(T, E, top_k, 1, 1, 1, score, bool(renormalize), logits.dtype is torch.bfloat16, float(scale))
+
+    def body(s):
+        d = nv._out(dlogits, "dlogits", logits.dtype, (T, E), dev)
+        nv._check(nv.lib().nvfp4_moe_gate_backward(c, logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
+                                                   d.data_ptr(), s), "nvfp4_moe_gate_backward")
+        return d
+    return nv._launch(dev, stream, body)
