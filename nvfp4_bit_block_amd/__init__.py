@@ -159,9 +159,10 @@ def _launch(device, stream, body):
     """body(stream handle) with `device` current and, when a stream is given,
     that stream (which must be one of the device's) as well, so that the
     body's temporaries and kernels share it.  Calls on the current device's
-    current stream, the common ones, skip the context managers (about 4 us)."""
+    current stream, the common ones, skip the context managers (about 4 us)
+    and the stream object (2.8 us against 0.1 us for its bare handle)."""
     if stream is None and device.index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream().cuda_stream)
+        return body(torch._C._cuda_getCurrentRawStream(device.index))
     if stream is not None and stream.device != device:
         raise ValueError(f"stream of {stream.device}, tensors on {device}")
     with torch.cuda.device(device):

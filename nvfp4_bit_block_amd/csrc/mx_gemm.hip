@@ -11,17 +11,17 @@
 // row: rows leave as whole pieces, and a block of 32 outputs of one row lies
 // in two lanes, which is what requantizing h needs.
 //
-// K step: 256 elements (128 code bytes, 8 scale bytes a row).  A K
-// permutation applied to both operands leaves the product unchanged: lane
-// half hf = lane / 32 takes blocks 4 hf + kk of the step in instruction kk, so
-// its four scale bytes are one word and byte kk is selected by the
-// instruction.
+// K step: 256 elements (128 code bytes, a cache line, and 8 scale bytes a
+// row), four instructions deep.  A K permutation applied to both operands
+// leaves the product unchanged: lane half hf = lane / 32 takes blocks
+// 4 hf + kk of the step in instruction kk, so its four scale bytes are one
+// word and byte kk is selected by the instruction.
 //
 // Codes go from global memory straight into LDS (buffer_load ... lds, 1 KB =
-// 8 rows per instruction), two stages, one barrier per step.  LDS rows are
-// not padded: row r keeps its 16-byte chunk c in slot c ^ ((r / 2) % 8), so
-// that 16 consecutive rows' fragment reads cover all banks.  Blocks past K
-// and rows past the operand load zeros with scale byte 0.
+// 8 rows per instruction) through NS stages, one barrier per step.  LDS rows
+// are not padded: row r keeps its 16-byte chunk c in slot c ^ ((r / 2) % 8),
+// so that 16 consecutive rows' fragment reads cover all banks.  Blocks past K
+// and rows past the operand load as zeros.
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 #include "nvfp4_dma.hpp"
@@ -32,6 +32,7 @@ namespace nvfp4 {
 
 namespace {
 
+constexpr int kWaitAll = vmcnt_imm(0) & ~0xF00;  // vector memory and LDS
 constexpr int kGroupM = 8;  // row tiles per band in the ungrouped tile order
 
 template <int SEL>
@@ -40,22 +41,25 @@ __device__ __forceinline__ f32x16 mfma_kk(u32x4 w, u32x4 a, f32x16 c, uint32_t s
 }
 
 // TM, TN: 32-row blocks of activations and of weights per wave; WM x WN
-// waves.  ALIGNED: K % 256 == 0, so a row's 8 scale bytes of a step are one
-// aligned word pair (else they are read byte by byte).
-template <int TM, int TN, int WM, int WN, MxEpi EP, bool ALIGNED>
+// waves; NS stages.  The activation blocks are dealt to the wave rows in turn
+// (wave row wm has blocks wm, wm + WM, ..), and a tile of fewer rows runs a
+// main loop of as many blocks as its fullest wave has.  ALIGNED: K % 128 == 0,
+// so a row's scale bytes are whole words (else they are read byte by byte).
+template <int TM, int TN, int WM, int WN, int NS, MxEpi EP, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     constexpr int NW = WM * WN, NT = 64 * NW;
-    constexpr int WTM = 32 * TM, WTN = 32 * TN, BM = WTM * WM, BN = WTN * WN;
-    constexpr int A_SLABS = BM / 8, B_SLABS = BN / 8;
-    constexpr int A_PER_W = A_SLABS / NW, B_PER_W = B_SLABS / NW;
-    static_assert(A_SLABS % NW == 0 && B_SLABS % NW == 0, "copy");
+    constexpr int WTN = 32 * TN, BM = 32 * TM * WM, BN = WTN * WN;
+    constexpr int SLABS = (BM + BN) / 8, CODES = SLABS / NW;  // code slabs of 1 KB: activations, then weights
+    static_assert(SLABS % NW == 0, "copy");
     constexpr int SC_OFF = (BM + BN) * 128;
     constexpr int STAGE = SC_OFF + (BM + BN) * 8;
+    constexpr int SC_SLABS = (BM + BN) / 32, SC_PER_W = (SC_SLABS + NW - 1) / NW;
     constexpr int SC_PER_T = (BM + BN + NT - 1) / NT;
-    static_assert(2 * STAGE <= 160 * 1024, "LDS");
+    constexpr int LOADS = CODES + (ALIGNED ? SC_PER_W : 0);  // of a wave, per step
+    static_assert(NS >= 2 && NS <= 3 && NS * STAGE <= 160 * 1024 && LOADS * (NS - 1) <= 63, "stages");
     constexpr bool kGateUp = EP == MxEpi::kGateUp;
     static_assert(!kGateUp || TN % 2 == 0, "gate/up pairs column blocks");
-    __shared__ __align__(1024) uint8_t smem[2 * STAGE];
+    __shared__ __align__(1024) uint8_t smem[NS * STAGE];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -76,15 +80,18 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     int grp = 0, tn;
     int64_t row_beg, row_end;
     if (g.groups > 0) {
+        // group by group, and within a group its row tiles of one column tile
+        // together: they read the same weights
         const int mt = (int)(id / g.ntiles);
-        tn = (int)(id - (int64_t)mt * g.ntiles);
         int lo = 0, hi = g.groups;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (g.tile_off[mid] <= mt) lo = mid; else hi = mid;
         }
         grp = lo;
-        row_beg = (int64_t)g.row_off[grp] + (int64_t)(mt - g.tile_off[grp]) * BM;
+        const int r = (int)(id - (int64_t)g.tile_off[grp] * g.ntiles), mts = g.tile_off[grp + 1] - g.tile_off[grp];
+        tn = r / mts;
+        row_beg = (int64_t)g.row_off[grp] + (int64_t)(r - tn * mts) * BM;
         row_end = min((int64_t)g.row_off[grp + 1], row_beg + BM);
     } else {
         const int64_t per_band = (int64_t)kGroupM * g.ntiles;
@@ -127,81 +134,95 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     const int64_t brows = (kGateUp ? 2 * nlim : nlim) - n0;
     const u32x4 rb = make_rsrc(g.b_codes + ((int64_t)grp * g.N + n0) * KB,
                                (uint64_t)(kGateUp || brows < BN ? brows : BN) * KB);
-    const uint8_t* const as = g.a_scales + a0 * KS;
-    const uint8_t* const bs = g.b_scales + ((int64_t)grp * g.N + n0) * KS;
 
-    // ---- copy assignments.  A code slab: tile rows 8 s + lane / 8, slot
-    // lane % 8, which holds chunk slot ^ ((r / 2) % 8).
-    uint32_t va[A_PER_W], vb[B_PER_W];
-    const int chunk0 = (lane & 7);
+    // ---- copy assignments.  Code slab sl: tile rows 8 sl + lane / 8 (the
+    // activations', then the weights'), slot lane % 8, which holds chunk
+    // slot ^ ((r / 2) % 8).
+    auto tile_row = [&](int r) -> int64_t { return r < BM ? a_row(r) : r < BM + BN ? b_row(r - BM) : -1; };
+    uint32_t vc[CODES];
+    // (r / 2) % 8 of row 8 sl + lane / 8 depends on sl's parity
+    const int slot = lane & 7, rhalf = lane >> 4;
 #pragma unroll
-    for (int u = 0; u < A_PER_W; ++u) {
-        const int r = 8 * (A_PER_W * wave + u) + (lane >> 3);
-        const int64_t src = a_row(r);
-        va[u] = src < 0 ? kOob : (uint32_t)src * KB + 16u * (chunk0 ^ ((r >> 1) & 7));
+    for (int u = 0; u < CODES; ++u) {
+        const int sl = CODES * wave + u;
+        const int64_t src = tile_row(8 * sl + (lane >> 3));
+        vc[u] = src < 0 ? kOob : (uint32_t)src * KB + 16u * (slot ^ (4 * (sl & 1) + rhalf));
     }
+    // scales.  ALIGNED: slab sl holds tile rows 32 sl + lane / 2, word lane %
+    // 2.  Otherwise thread t carries tile rows t, t + NT, .. of one step
+    // through registers.
+    const u32x4 rsa = make_rsrc(g.a_scales + a0 * KS, (uint64_t)(gather ? g.a_src_rows : row_end - row_beg) * KS);
+    const u32x4 rsb = make_rsrc(g.b_scales + ((int64_t)grp * g.N + n0) * KS,
+                                (uint64_t)(kGateUp || brows < BN ? brows : BN) * KS);
+    // (slabs beyond an even deal repeat the last one)
+    auto sc_slab = [&](int u) { return min(SC_PER_W * wave + u, SC_SLABS - 1); };
+    uint32_t vs[ALIGNED ? SC_PER_W : 1];
+    const uint8_t* sp[ALIGNED ? 1 : SC_PER_T];
+    bool sok[ALIGNED ? 1 : SC_PER_T];
+    uint2 sv[ALIGNED ? 1 : SC_PER_T];
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int u = 0; u < B_PER_W; ++u) {
-        const int r = 8 * (B_PER_W * wave + u) + (lane >> 3);
-        const int64_t src = b_row(r);
-        vb[u] = src < 0 ? kOob : (uint32_t)src * KB + 16u * (chunk0 ^ ((r >> 1) & 7));
-    }
-    // scales: thread t handles tile rows t, t + NT, ..: activations, then weights
-    const uint8_t* sp[SC_PER_T];
+        for (int u = 0; u < SC_PER_W; ++u) {
+            const int64_t src = tile_row(32 * sc_slab(u) + (lane >> 1));
+            vs[u] = src < 0 ? kOob : (uint32_t)src * KS + 4u * (lane & 1);
+        }
+    } else {
+        const uint8_t* const as = g.a_scales + a0 * KS;
+        const uint8_t* const bs = g.b_scales + ((int64_t)grp * g.N + n0) * KS;
 #pragma unroll
-    for (int u = 0; u < SC_PER_T; ++u) {
-        const int r = tid + u * NT;
-        sp[u] = nullptr;
-        if (r < BM) {
-            const int64_t src = a_row(r);
-            if (src >= 0) sp[u] = as + src * KS;
-        } else if (r < BM + BN) {
-            const int64_t src = b_row(r - BM);
-            if (src >= 0) sp[u] = bs + src * KS;
+        for (int u = 0; u < SC_PER_T; ++u) {
+            const int r = tid + u * NT;
+            const int64_t src = tile_row(r);
+            sp[u] = (r < BM ? as : bs) + max(src, (int64_t)0) * KS;  // (a row that is there, if none is meant)
+            sok[u] = src >= 0;
         }
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
-    uint2 sv[SC_PER_T];
     auto load_scales = [&](int kc) {
+        if constexpr (!ALIGNED) {
+            const int nb = kc + 1 < nsteps ? 8 : tail;
 #pragma unroll
-        for (int u = 0; u < SC_PER_T; ++u) {
-            sv[u] = make_uint2(0, 0);
-            if (sp[u] == nullptr) continue;
-            if constexpr (ALIGNED) {
-                sv[u] = *reinterpret_cast<const uint2*>(sp[u] + 8 * kc);
-            } else {
-                const int nb = kc + 1 < nsteps ? 8 : tail;
+            for (int u = 0; u < SC_PER_T; ++u) {
                 uint32_t w[2] = {0, 0};
 #pragma unroll
-                for (int b = 0; b < 8; ++b)
-                    if (b < nb) w[b >> 2] |= (uint32_t)sp[u][8 * kc + b] << (8 * (b & 3));
+                for (int b = 0; b < 8; ++b) {
+                    const uint32_t v = sp[u][8 * kc + min(b, nb - 1)];
+                    w[b >> 2] |= (sok[u] && b < nb ? v : 0u) << (8 * (b & 3));
+                }
                 sv[u] = make_uint2(w[0], w[1]);
             }
         }
     };
-    auto store_scales = [&](int st) {
+    auto store_scales = [&](uint32_t stage) {
+        if constexpr (!ALIGNED) {
 #pragma unroll
-        for (int u = 0; u < SC_PER_T; ++u) {
-            const int r = tid + u * NT;
-            if (r < BM + BN) *reinterpret_cast<uint2*>(smem + st * STAGE + SC_OFF + 8 * r) = sv[u];
+            for (int u = 0; u < SC_PER_T; ++u) {
+                const int r = tid + u * NT;
+                if (r < BM + BN) *reinterpret_cast<uint2*>(smem + stage + SC_OFF + 8 * r) = sv[u];
+            }
         }
     };
-    auto issue = [&](int kc, int st) {
-        const uint32_t b = lds0 + (uint32_t)(st * STAGE);
-        const bool cut = !ALIGNED && kc + 1 == nsteps;  // the last step may lack blocks
-#pragma unroll
-        for (int u = 0; u < A_PER_W; ++u) {
-            const int sl = A_PER_W * wave + u;
-            uint32_t v = va[u];
-            if (cut && (chunk0 ^ (((8 * sl + (lane >> 3)) >> 1) & 7)) >= tail) v = kOob;
-            lds_load16(ra, v, (uint32_t)kc * 128u, b + (uint32_t)(sl * 1024));
-        }
-#pragma unroll
-        for (int u = 0; u < B_PER_W; ++u) {
-            const int sl = B_PER_W * wave + u;
-            uint32_t v = vb[u];
-            if (cut && (chunk0 ^ (((8 * sl + (lane >> 3)) >> 1) & 7)) >= tail) v = kOob;
-            lds_load16(rb, v, (uint32_t)kc * 128u, b + (uint32_t)(BM * 128 + sl * 1024));
+    // Load p (0 .. LOADS - 1) of this wave for step kc into a stage.  In the
+    // last step the chunks (and scale words) past K are pushed out of range,
+    // and steps past the last load nothing: a resource of no bytes, at offset
+    // zero so that the range check holds whichever way it counts the offset.
+    auto issue = [&](int p, int kc, uint32_t stage) {
+        const bool live = kc < nsteps, last = kc + 1 == nsteps;
+        const bool code = p < CODES;
+        const int sl = code ? CODES * wave + p : sc_slab(p - CODES);
+        const bool isa = code ? 8 * sl < BM : 32 * sl < BM;
+        u32x4 r = code ? (isa ? ra : rb) : (isa ? rsa : rsb);
+        r.x = __builtin_amdgcn_readfirstlane(r.x);
+        r.y = __builtin_amdgcn_readfirstlane(r.y);
+        r.z = __builtin_amdgcn_readfirstlane(live ? r.z : 0u);
+        r.w = kRsrcWord3;
+        const uint32_t k = live ? (uint32_t)kc : 0u;
+        if (code) {
+            const uint32_t cut = last && (slot ^ (4 * (sl & 1) + rhalf)) >= tail ? kOob : 0u;
+            lds_load16(r, vc[code ? p : 0] | cut, k * 128u, lds0 + stage + (uint32_t)(sl * 1024));
+        } else {
+            const uint32_t cut = last && 4 * (lane & 1) >= tail ? kOob : 0u;
+            lds_load4(r, vs[code ? 0 : p - CODES] | cut, k * 8u, lds0 + stage + (uint32_t)(SC_OFF + 256 * sl));
         }
     };
 
@@ -213,61 +234,111 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
 
+    // ---- main loop.  The fragments of the next instruction are read among
+    // the instructions of this one, into the other half of the fragment
+    // registers.  The step's barrier stands before its last quarter: by then
+    // every fragment of the step is in registers, so the stage is free, and
+    // the next step has landed (only the loads of the steps after it may be
+    // out); the last quarter's instructions cover the first reads of the next
+    // step and the issue of the loads into the freed stage.  The scheduling
+    // barriers keep that order, and the body must not branch: the matrix
+    // instructions, which the compiler sees without side effects, otherwise
+    // sink below the last branch and nothing overlaps (325 us against 239 us
+    // at 4096 x 6144 x 16384, tiles of 256 x 256).
     uint32_t off_k[4];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) off_k[kk] = (uint32_t)(c32 * 128 + 16 * ((4 * hf + kk) ^ ((c32 >> 1) & 7)));
-    auto compute = [&](int st) {
-        const uint8_t* const base = smem + st * STAGE;
-        const uint8_t* const ab = base + wm * WTM * 128;
-        const uint8_t* const bb = base + BM * 128 + wn * WTN * 128;
-        const uint8_t* const sab = base + SC_OFF + 8 * (wm * WTM + c32) + 4 * hf;
-        const uint8_t* const sbb = base + SC_OFF + 8 * (BM + wn * WTN + c32) + 4 * hf;
-        uint32_t sa[TM], sb[TN];
+    const uint32_t a_off = (uint32_t)(wm * 32 * 128), b_off = (uint32_t)((BM + wn * WTN) * 128);
+    const uint32_t sa_off = (uint32_t)(SC_OFF + 8 * (32 * wm + c32) + 4 * hf);
+    const uint32_t sb_off = (uint32_t)(SC_OFF + 8 * (BM + wn * WTN + c32) + 4 * hf);
+    load_scales(0);
+    store_scales(0);
+    load_scales(min(1, nsteps - 1));
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(sab + 256 * i);
+    for (int t = 0; t < NS; ++t)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) sb[j] = *reinterpret_cast<const uint32_t*>(sbb + 256 * j);
-        auto group = [&](auto kkc) {
-            constexpr int kk = decltype(kkc)::value;
-            u32x4 a[TM], b[TN];
+        for (int p = 0; p < LOADS; ++p) issue(p, t, t * STAGE);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (NS - 1)) & ~0xF00);
+    __syncthreads();
+    auto main_loop = [&](auto tmc) {
+        constexpr int TA = decltype(tmc)::value;  // activation blocks in use
+        u32x4 fa[2][TA], fb[2][TN];
+        uint32_t sa[TA], sb[TN];
+        auto read_frag = [&](int q, uint32_t stage, int kk, int buf) {  // q: 0 .. TA + TN - 1
+            if (q < TA)
+                fa[buf][q] = *reinterpret_cast<const u32x4*>(smem + (stage + off_k[kk] + a_off) + 4096 * WM * q);
+            else
+                fb[buf][q - TA] = *reinterpret_cast<const u32x4*>(smem + (stage + off_k[kk] + b_off) + 4096 * (q - TA));
+        };
+        auto read_scales = [&](uint32_t stage, uint32_t (&da)[TA], uint32_t (&db)[TN]) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) a[i] = *reinterpret_cast<const u32x4*>(ab + off_k[kk] + 4096 * i);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) b[j] = *reinterpret_cast<const u32x4*>(bb + off_k[kk] + 4096 * j);
+            for (int i = 0; i < TA; ++i)
+                da[i] = *reinterpret_cast<const uint32_t*>(smem + (stage + sa_off) + 256 * WM * i);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int i = 0; i < TM; ++i) acc[j][i] = mfma_kk<kk>(b[j], a[i], acc[j][i], sb[j], sa[i]);
+                db[j] = *reinterpret_cast<const uint32_t*>(smem + (stage + sb_off) + 256 * j);
         };
-        group(std::integral_constant<int, 0>{});
-        group(std::integral_constant<int, 1>{});
-        group(std::integral_constant<int, 2>{});
-        group(std::integral_constant<int, 3>{});
-    };
-
-    load_scales(0);
-    issue(0, 0);
-    store_scales(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __syncthreads();
-    for (int s = 0; s < nsteps; ++s) {
-        const int st = s & 1;
-        const bool more = s + 1 < nsteps;
-        if (more) {
-            load_scales(s + 1);
-            issue(s + 1, st ^ 1);
+        read_scales(0, sa, sb);
+#pragma unroll
+        for (int q = 0; q < TA + TN; ++q) read_frag(q, 0, 0, 0);
+        uint32_t cur = 0;
+        for (int s = 0; s < nsteps; ++s) {
+            const uint32_t nxt = cur + STAGE == NS * STAGE ? 0 : cur + STAGE;
+            uint32_t na[TA], nb[TN];
+            auto group = [&](auto kkc) {
+                constexpr int kk = decltype(kkc)::value, buf = kk & 1;
+                if constexpr (kk == 3) {
+                    __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (NS - 2)) & ~0xF00);
+                    store_scales(nxt);
+                    __syncthreads();
+                    read_scales(nxt, na, nb);
+                    load_scales(min(s + 2, nsteps - 1));
+                }
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    constexpr int kR = (TA + TN + TN - 1) / TN, kL = (LOADS + TN - 1) / TN;
+#pragma unroll
+                    for (int q = j * kR; q < (j + 1) * kR && q < TA + TN; ++q)
+                        read_frag(q, kk < 3 ? cur : nxt, (kk + 1) & 3, buf ^ 1);
+#pragma unroll
+                    for (int i = 0; i < TA; ++i)
+                        acc[j][i] = mfma_kk<kk>(fb[buf][j], fa[buf][i], acc[j][i], sb[j], sa[i]);
+                    if constexpr (kk == 3) {
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int p = j * kL; p < (j + 1) * kL && p < LOADS; ++p) issue(p, s + NS, cur);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            group(std::integral_constant<int, 0>{});
+            group(std::integral_constant<int, 1>{});
+            group(std::integral_constant<int, 2>{});
+            group(std::integral_constant<int, 3>{});
+#pragma unroll
+            for (int i = 0; i < TA; ++i) sa[i] = na[i];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) sb[j] = nb[j];
+            cur = nxt;
         }
-        compute(st);
-        if (more) store_scales(st ^ 1);
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-        __syncthreads();
-    }
+    };
+    // blocks of the fullest wave row
+    const int used = (int)((row_end - row_beg + 32 * WM - 1) / (32 * WM));
+    if (TM >= 2 && used == 1) main_loop(std::integral_constant<int, 1>{});
+    else if (TM >= 3 && used == 2) main_loop(std::integral_constant<int, TM >= 3 ? 2 : TM>{});
+    else if (TM >= 4 && used == 3) main_loop(std::integral_constant<int, TM >= 4 ? 3 : TM>{});
+    else main_loop(std::integral_constant<int, TM>{});
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+
+    // (the slabs below reuse the stages, which other waves may still read)
+    if constexpr (EP == MxEpi::kStoreBf16) __syncthreads();
 
     // ---- epilogue: acc[j][i][r] is weight row 32 j + 8 (r / 4) + 4 hf + r % 4
-    // of the wave, activation row 32 i + c32.
+    // of the wave, activation row 32 (i WM + wm) + c32.
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int64_t row = row_beg + wm * WTM + 32 * i + c32;
+        const int64_t row = row_beg + 32 * (i * WM + wm) + c32;
         if constexpr (kGateUp) {
             // (rows past the end take part in the exchange and store nothing)
 #pragma unroll
@@ -299,40 +370,57 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
                     if (hf == 0) g.out_scales[row * (g.ldo / 32) + hc / 32] = (uint8_t)s;
                 }
             }
-        } else {
+        } else if constexpr (EP == MxEpi::kDown) {
             if (row >= row_end) continue;
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
+                    // (N is the hidden size, a multiple of 32)
                     const int64_t col = n0 + wn * WTN + 32 * j + 8 * p + 4 * hf;
-                    if (col >= nlim) continue;
-                    const float v0 = acc[j][i][4 * p], v1 = acc[j][i][4 * p + 1], v2 = acc[j][i][4 * p + 2],
-                                v3 = acc[j][i][4 * p + 3];
-                    if constexpr (EP == MxEpi::kDown) {
-                        // (N is the hidden size, a multiple of 32)
-                        *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.out) + row * g.ldo + col) =
-                            make_float4(v0, v1, v2, v3);
-                    } else {
-                        uint16_t* const dst = reinterpret_cast<uint16_t*>(g.out) + row * g.ldo + col;
-                        const uint32_t lo = f32_to_bf16(v0) | (f32_to_bf16(v1) << 16);
-                        const uint32_t hi = f32_to_bf16(v2) | (f32_to_bf16(v3) << 16);
-                        if ((g.ldo & 3) == 0) {
-                            *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
-                        } else {
-                            dst[0] = (uint16_t)lo;
-                            if (col + 1 < nlim) dst[1] = (uint16_t)(lo >> 16);
-                            if (col + 2 < nlim) dst[2] = (uint16_t)hi;
-                            if (col + 3 < nlim) dst[3] = (uint16_t)(hi >> 16);
-                        }
-                    }
+                    if (col < nlim)
+                        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(g.out) + row * g.ldo + col) =
+                            f32x4{acc[j][i][4 * p], acc[j][i][4 * p + 1], acc[j][i][4 * p + 2], acc[j][i][4 * p + 3]};
+                }
+        } else {
+            // a 32-row slab of the wave's tile meets in LDS and leaves as
+            // 16-byte pieces of rows (pitch: 16 rows' 8-byte writes fall on
+            // different banks)
+            constexpr int kPitch = WTN * 2 + 16;
+            static_assert(NW * 32 * kPitch <= NS * STAGE, "epilogue slabs");
+            uint8_t* const slab = smem + wave * 32 * kPitch;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    *reinterpret_cast<uint2*>(slab + c32 * kPitch + 2 * (32 * j + 8 * p + 4 * hf)) =
+                        make_uint2(f32_to_bf16(acc[j][i][4 * p]) | (f32_to_bf16(acc[j][i][4 * p + 1]) << 16),
+                                   f32_to_bf16(acc[j][i][4 * p + 2]) | (f32_to_bf16(acc[j][i][4 * p + 3]) << 16));
+            __builtin_amdgcn_wave_barrier();
+            const int64_t row0 = row_beg + 32 * (i * WM + wm);
+            const bool vec = (g.ldo & 7) == 0;
+#pragma unroll
+            for (int p = 0; p < 2 * TN; ++p) {
+                const int e = 64 * p + lane, rr = e / (4 * TN), ch = e % (4 * TN);
+                const uint4 v = *reinterpret_cast<const uint4*>(slab + rr * kPitch + 16 * ch);
+                const int64_t col = n0 + wn * WTN + 8 * ch;
+                if (row0 + rr >= row_end || col >= nlim) continue;
+                uint16_t* const dst = reinterpret_cast<uint16_t*>(g.out) + (row0 + rr) * g.ldo + col;
+                if (vec && col + 8 <= nlim) {
+                    *reinterpret_cast<uint4*>(dst) = v;
+                } else {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (col + q < nlim) dst[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
                 }
             }
+            __builtin_amdgcn_wave_barrier();
         }
     }
 }
 
-template <int TM, int TN, int WM, int WN, MxEpi EP>
+template <int TM, int TN, int WM, int WN, int NS, MxEpi EP>
 hipError_t launch_cfg(const MxGemmArgs& g0, int grid_m, hipStream_t stream) {
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
     MxGemmArgs g = g0;
@@ -342,10 +430,10 @@ hipError_t launch_cfg(const MxGemmArgs& g0, int grid_m, hipStream_t stream) {
     int64_t wgs = mt * g.ntiles;
     if (g.groups > 0) wgs = (wgs + 7) / 8 * 8;  // a multiple of 8 for the XCD renumbering
     if (wgs < 1 || wgs >= ((int64_t)1 << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
-    if (g.K % 256 == 0)
-        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, EP, true>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
+    if (g.K % 128 == 0)
+        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, NS, EP, true>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
     else
-        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, EP, false>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
+        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, NS, EP, false>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
     return hipGetLastError();
 }
 
@@ -353,9 +441,9 @@ hipError_t launch_cfg(const MxGemmArgs& g0, int grid_m, hipStream_t stream) {
 
 hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream) {
     switch (epi) {
-        case MxEpi::kStoreBf16: return launch_cfg<2, 2, 2, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
-        case MxEpi::kGateUp: return launch_cfg<2, 2, 2, 2, MxEpi::kGateUp>(g, grid_m, stream);
-        default: return launch_cfg<2, 2, 2, 2, MxEpi::kDown>(g, grid_m, stream);
+        case MxEpi::kStoreBf16: return launch_cfg<2, 2, 2, 2, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
+        case MxEpi::kGateUp: return launch_cfg<2, 2, 2, 2, 2, MxEpi::kGateUp>(g, grid_m, stream);
+        default: return launch_cfg<2, 2, 2, 2, 2, MxEpi::kDown>(g, grid_m, stream);
     }
 }
 
