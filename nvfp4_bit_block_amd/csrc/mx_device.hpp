@@ -52,6 +52,21 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t m, uint32_t w) {
     return max(max(m, w & 0x7FFFu), (w >> 16) & 0x7FFFu);
 }
 
+// The group whose row tiles [tile_off[e], tile_off[e + 1]) hold tile `mt`
+// (which some group's do): a wave compares 64 bounds at a time, so 4096
+// groups take two dependent loads.
+__device__ __forceinline__ int group_of_tile(const int32_t* __restrict__ tile_off, int groups, int mt) {
+    const int lane = threadIdx.x & 63, stride = (groups + 63) / 64;
+    int lo = 0, e = lane * stride;
+    if (stride > 1) {
+        const bool le = e < groups && tile_off[e] <= mt;
+        lo = (__popcll(__ballot(le)) - 1) * stride;  // the bounds ascend; tile_off[0] = 0
+    }
+    e = lo + lane;
+    const bool le = lane < stride + (stride == 1 ? 63 : 0) && e < groups && tile_off[e] <= mt;
+    return __builtin_amdgcn_readfirstlane(lo + __popcll(__ballot(le)) - 1);
+}
+
 // D += A B on the scaled matrix instructions.  32x32x64: lane l holds row
 // (column) l % 32 and the 32 K positions [32 (l / 32), + 32), one MX block,
 // as 16 code bytes; 16x16x128: row l % 16, block l / 16.  Byte SEL of the

@@ -20,8 +20,10 @@
 // Codes go from global memory straight into LDS (buffer_load ... lds, 1 KB =
 // 8 rows per instruction) through NS stages, one barrier per step.  LDS rows
 // are not padded: row r keeps its 16-byte chunk c in slot c ^ ((r / 2) % 8),
-// so that 16 consecutive rows' fragment reads cover all banks.  Blocks past K
-// and rows past the operand load as zeros.
+// so that 16 consecutive rows' fragment reads cover all banks.  A step's 8
+// scale bytes of a row would cost a request to L2 like the 128 bytes of its
+// codes; they come 32 at a time, for four steps, into a ring of their own.
+// Blocks past K and rows past the operand load as zeros.
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 #include "nvfp4_dma.hpp"
@@ -44,22 +46,26 @@ __device__ __forceinline__ f32x16 mfma_kk(u32x4 w, u32x4 a, f32x16 c, uint32_t s
 // waves; NS stages.  The activation blocks are dealt to the wave rows in turn
 // (wave row wm has blocks wm, wm + WM, ..), and a tile of fewer rows runs a
 // main loop of as many blocks as its fullest wave has.  ALIGNED: K % 128 == 0,
-// so a row's scale bytes are whole words (else they are read byte by byte).
+// so a row's scale bytes are whole words (else each step's are shifted into
+// place on their way through registers).
 template <int TM, int TN, int WM, int WN, int NS, MxEpi EP, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     constexpr int NW = WM * WN, NT = 64 * NW;
     constexpr int WTN = 32 * TN, BM = 32 * TM * WM, BN = WTN * WN;
-    constexpr int SLABS = (BM + BN) / 8, CODES = SLABS / NW;  // code slabs of 1 KB: activations, then weights
-    static_assert(SLABS % NW == 0, "copy");
-    constexpr int SC_OFF = (BM + BN) * 128;
-    constexpr int STAGE = SC_OFF + (BM + BN) * 8;
-    constexpr int SC_SLABS = (BM + BN) / 32, SC_PER_W = (SC_SLABS + NW - 1) / NW;
+    constexpr int SLABS = (BM + BN) / 8, CODES = (SLABS + NW - 1) / NW;  // code slabs of 1 KB: activations, then weights
+    constexpr int STAGE = (BM + BN) * 128;
+    // scale ring: two halves, each four steps' 32 bytes of every row; slabs of
+    // 32 rows (1 KB), one per wave and phase
+    constexpr int SC_OFF = NS * STAGE, SC_HALF = (BM + BN) * 32;
+    constexpr int SC_SLABS = (BM + BN) / 32, PHASES = (SC_SLABS + NW - 1) / NW;
     constexpr int SC_PER_T = (BM + BN + NT - 1) / NT;
-    constexpr int LOADS = CODES + (ALIGNED ? SC_PER_W : 0);  // of a wave, per step
-    static_assert(NS >= 2 && NS <= 3 && NS * STAGE <= 160 * 1024 && LOADS * (NS - 1) <= 63, "stages");
+    constexpr int LOADS = CODES + (ALIGNED ? 1 : 0);  // of a wave, per step
+    static_assert(NS >= 2 && NS <= 3 && PHASES <= (NS == 2 ? 4 : 3) && LOADS * (NS - 1) <= 63, "stages");
+    constexpr int LDS = SC_OFF + 2 * SC_HALF;
+    static_assert(LDS <= 160 * 1024, "LDS");
     constexpr bool kGateUp = EP == MxEpi::kGateUp;
     static_assert(!kGateUp || TN % 2 == 0, "gate/up pairs column blocks");
-    __shared__ __align__(1024) uint8_t smem[NS * STAGE];
+    __shared__ __align__(1024) uint8_t smem[LDS];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -82,13 +88,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     if (g.groups > 0) {
         // group by group, and within a group its row tiles of one column tile
         // together: they read the same weights
-        const int mt = (int)(id / g.ntiles);
-        int lo = 0, hi = g.groups;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (g.tile_off[mid] <= mt) lo = mid; else hi = mid;
-        }
-        grp = lo;
+        grp = group_of_tile(g.tile_off, g.groups, (int)(id / g.ntiles));
         const int r = (int)(id - (int64_t)g.tile_off[grp] * g.ntiles), mts = g.tile_off[grp + 1] - g.tile_off[grp];
         tn = r / mts;
         row_beg = (int64_t)g.row_off[grp] + (int64_t)(r - tn * mts) * BM;
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     }
 
     const uint32_t KB = (uint32_t)(g.K / 2), KS = (uint32_t)(g.K / 32);
-    const int nsteps = (int)((g.K + 255) / 256);
+    const int nsteps = (int)((KS + 7) / 8);
     const int tail = (int)(KS - 8 * (uint32_t)(nsteps - 1));  // blocks of the last step, 1 .. 8
 
     // First weight row of the tile, and tile row n's row relative to it (-1
@@ -136,94 +136,103 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
                                (uint64_t)(kGateUp || brows < BN ? brows : BN) * KB);
 
     // ---- copy assignments.  Code slab sl: tile rows 8 sl + lane / 8 (the
-    // activations', then the weights'), slot lane % 8, which holds chunk
-    // slot ^ ((r / 2) % 8).
+    // activations', then the weights'), slot lane % 8.
     auto tile_row = [&](int r) -> int64_t { return r < BM ? a_row(r) : r < BM + BN ? b_row(r - BM) : -1; };
+    // the chunk in this lane's slot of slab sl
+    auto chunk_of = [&](int sl) { return (lane & 7) ^ (((8 * sl + (lane >> 3)) >> 1) & 7); };
+    // (slabs beyond an even deal repeat the last one)
+    auto slab = [&](int u) { return SLABS % NW == 0 ? CODES * wave + u : min(CODES * wave + u, SLABS - 1); };
     uint32_t vc[CODES];
-    // (r / 2) % 8 of row 8 sl + lane / 8 depends on sl's parity
-    const int slot = lane & 7, rhalf = lane >> 4;
 #pragma unroll
     for (int u = 0; u < CODES; ++u) {
-        const int sl = CODES * wave + u;
+        const int sl = slab(u);
         const int64_t src = tile_row(8 * sl + (lane >> 3));
-        vc[u] = src < 0 ? kOob : (uint32_t)src * KB + 16u * (slot ^ (4 * (sl & 1) + rhalf));
+        vc[u] = src < 0 ? kOob : (uint32_t)src * KB + 16u * chunk_of(sl);
     }
-    // scales.  ALIGNED: slab sl holds tile rows 32 sl + lane / 2, word lane %
-    // 2.  Otherwise thread t carries tile rows t, t + NT, .. of one step
-    // through registers.
-    const u32x4 rsa = make_rsrc(g.a_scales + a0 * KS, (uint64_t)(gather ? g.a_src_rows : row_end - row_beg) * KS);
-    const u32x4 rsb = make_rsrc(g.b_scales + ((int64_t)grp * g.N + n0) * KS,
-                                (uint64_t)(kGateUp || brows < BN ? brows : BN) * KS);
-    // (slabs beyond an even deal repeat the last one)
-    auto sc_slab = [&](int u) { return min(SC_PER_W * wave + u, SC_SLABS - 1); };
-    uint32_t vs[ALIGNED ? SC_PER_W : 1];
-    const uint8_t* sp[ALIGNED ? 1 : SC_PER_T];
-    bool sok[ALIGNED ? 1 : SC_PER_T];
+    // scales.  ALIGNED: slab sl holds tile rows 32 sl + lane / 2, half lane % 2
+    // of their 32 bytes; in phase p a wave loads slab p NW + wave.  Otherwise
+    // thread t carries tile rows t, t + NT, .. of one step through registers,
+    // from a base rounded down to a word.
+    const uint8_t* const as = g.a_scales + a0 * KS;
+    const uint8_t* const bs = g.b_scales + ((int64_t)grp * g.N + n0) * KS;
+    const uint32_t da = ALIGNED ? 0u : (uint32_t)(uintptr_t)as & 3u, db = ALIGNED ? 0u : (uint32_t)(uintptr_t)bs & 3u;
+    const u32x4 rsa = make_rsrc(as - da, ((uint64_t)(gather ? g.a_src_rows : row_end - row_beg) * KS + da + 3) & ~3ull);
+    const u32x4 rsb = make_rsrc(bs - db, ((uint64_t)(kGateUp || brows < BN ? brows : BN) * KS + db + 3) & ~3ull);
+    uint32_t vs[ALIGNED ? PHASES : SC_PER_T];
     uint2 sv[ALIGNED ? 1 : SC_PER_T];
-    if constexpr (ALIGNED) {
 #pragma unroll
-        for (int u = 0; u < SC_PER_W; ++u) {
-            const int64_t src = tile_row(32 * sc_slab(u) + (lane >> 1));
-            vs[u] = src < 0 ? kOob : (uint32_t)src * KS + 4u * (lane & 1);
-        }
-    } else {
-        const uint8_t* const as = g.a_scales + a0 * KS;
-        const uint8_t* const bs = g.b_scales + ((int64_t)grp * g.N + n0) * KS;
-#pragma unroll
-        for (int u = 0; u < SC_PER_T; ++u) {
-            const int r = tid + u * NT;
-            const int64_t src = tile_row(r);
-            sp[u] = (r < BM ? as : bs) + max(src, (int64_t)0) * KS;  // (a row that is there, if none is meant)
-            sok[u] = src >= 0;
-        }
+    for (int u = 0; u < (ALIGNED ? PHASES : SC_PER_T); ++u) {
+        const int r = ALIGNED ? 32 * (u * NW + wave) + (lane >> 1) : tid + u * NT;
+        const int64_t src = tile_row(r);
+        vs[u] = src < 0 ? kOob : (uint32_t)src * KS + (ALIGNED ? 16u * (lane & 1) : r < BM ? da : db);
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
+    // Phase ph of the scales of steps 4 q .. 4 q + 3 (phases and slabs that do
+    // not exist repeat one that does).  The 32 bytes may run past the row,
+    // whose neighbour's bytes no step uses, and past the tensor, where the
+    // range check, made word by word, gives zeros.
+    auto issue_scales = [&](int ph, int q) {
+        if constexpr (ALIGNED) {
+            ph = min(ph, PHASES - 1);
+            int sl = ph * NW + wave;
+            uint32_t v = vs[0];
+#pragma unroll
+            for (int u = 1; u < PHASES; ++u) v = ph == u ? vs[u] : v;
+            if (SC_SLABS % NW != 0 && sl >= SC_SLABS) {
+                sl = wave;
+                v = vs[0];
+            }
+            const bool isa = 32 * sl < BM;
+            u32x4 r = isa ? rsa : rsb;
+            r.x = __builtin_amdgcn_readfirstlane(r.x);
+            r.y = __builtin_amdgcn_readfirstlane(r.y);
+            r.z = __builtin_amdgcn_readfirstlane(r.z);
+            r.w = kRsrcWord3;
+            lds_load16(r, v + 32u * (uint32_t)q, 0u, lds0 + (uint32_t)(SC_OFF + (q & 1) * SC_HALF + 1024 * sl));
+        }
+    };
     auto load_scales = [&](int kc) {
         if constexpr (!ALIGNED) {
             const int nb = kc + 1 < nsteps ? 8 : tail;
+            const uint32_t m0 = nb >= 4 ? ~0u : (1u << (8 * nb)) - 1u;
+            const uint32_t m1 = nb >= 8 ? ~0u : nb <= 4 ? 0u : (1u << (8 * (nb - 4))) - 1u;
 #pragma unroll
             for (int u = 0; u < SC_PER_T; ++u) {
-                uint32_t w[2] = {0, 0};
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    const uint32_t v = sp[u][8 * kc + min(b, nb - 1)];
-                    w[b >> 2] |= (sok[u] && b < nb ? v : 0u) << (8 * (b & 3));
-                }
-                sv[u] = make_uint2(w[0], w[1]);
+                // (rows of one wave are all activations or all weights)
+                const u32x4 rr = __builtin_amdgcn_readfirstlane(tid + u * NT) < BM ? rsa : rsb;
+                const uint32_t at = vs[u] + 8u * (uint32_t)kc, sh = 8u * (at & 3u);
+                const u32x4 d = __builtin_amdgcn_raw_buffer_load_b128(
+                    __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)rr.y << 32) | rr.x), 0, (int)rr.z, (int)rr.w),
+                    (int)(at & ~3u), 0, 0);
+                sv[u].x = __builtin_amdgcn_alignbit(d.y, d.x, sh) & m0;
+                sv[u].y = __builtin_amdgcn_alignbit(d.z, d.y, sh) & m1;
             }
         }
     };
-    auto store_scales = [&](uint32_t stage) {
+    auto store_scales = [&](int kc) {
         if constexpr (!ALIGNED) {
 #pragma unroll
             for (int u = 0; u < SC_PER_T; ++u) {
                 const int r = tid + u * NT;
-                if (r < BM + BN) *reinterpret_cast<uint2*>(smem + stage + SC_OFF + 8 * r) = sv[u];
+                if (r < BM + BN)
+                    *reinterpret_cast<uint2*>(smem + SC_OFF + ((kc >> 2) & 1) * SC_HALF + 32 * r + 8 * (kc & 3)) = sv[u];
             }
         }
     };
-    // Load p (0 .. LOADS - 1) of this wave for step kc into a stage.  In the
-    // last step the chunks (and scale words) past K are pushed out of range,
-    // and steps past the last load nothing: a resource of no bytes, at offset
-    // zero so that the range check holds whichever way it counts the offset.
+    // Code load p (0 .. CODES - 1) of this wave for step kc into a stage.  In
+    // the last step the chunks past K are pushed out of range, and steps past
+    // the last load nothing: a resource of no bytes, at offset zero so that
+    // the range check holds whichever way it counts the offset.
     auto issue = [&](int p, int kc, uint32_t stage) {
         const bool live = kc < nsteps, last = kc + 1 == nsteps;
-        const bool code = p < CODES;
-        const int sl = code ? CODES * wave + p : sc_slab(p - CODES);
-        const bool isa = code ? 8 * sl < BM : 32 * sl < BM;
-        u32x4 r = code ? (isa ? ra : rb) : (isa ? rsa : rsb);
+        const int sl = slab(p);
+        u32x4 r = 8 * sl < BM ? ra : rb;
         r.x = __builtin_amdgcn_readfirstlane(r.x);
         r.y = __builtin_amdgcn_readfirstlane(r.y);
         r.z = __builtin_amdgcn_readfirstlane(live ? r.z : 0u);
         r.w = kRsrcWord3;
-        const uint32_t k = live ? (uint32_t)kc : 0u;
-        if (code) {
-            const uint32_t cut = last && (slot ^ (4 * (sl & 1) + rhalf)) >= tail ? kOob : 0u;
-            lds_load16(r, vc[code ? p : 0] | cut, k * 128u, lds0 + stage + (uint32_t)(sl * 1024));
-        } else {
-            const uint32_t cut = last && 4 * (lane & 1) >= tail ? kOob : 0u;
-            lds_load4(r, vs[code ? 0 : p - CODES] | cut, k * 8u, lds0 + stage + (uint32_t)(SC_OFF + 256 * sl));
-        }
+        const uint32_t cut = last && chunk_of(sl) >= tail ? kOob : 0u;
+        lds_load16(r, vc[p] | cut, live ? (uint32_t)kc * 128u : 0u, lds0 + stage + (uint32_t)(sl * 1024));
     };
 
     f32x16 acc[TN][TM];
@@ -236,10 +245,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
 
     // ---- main loop.  The fragments of the next instruction are read among
     // the instructions of this one, into the other half of the fragment
-    // registers.  The step's barrier stands before its last quarter: by then
+    // registers.  The step's barrier stands before its last instructions: by then
     // every fragment of the step is in registers, so the stage is free, and
     // the next step has landed (only the loads of the steps after it may be
-    // out); the last quarter's instructions cover the first reads of the next
+    // out); those last instructions cover the first reads of the next
     // step and the issue of the loads into the freed stage.  The scheduling
     // barriers keep that order, and the body must not branch: the matrix
     // instructions, which the compiler sees without side effects, otherwise
@@ -249,15 +258,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) off_k[kk] = (uint32_t)(c32 * 128 + 16 * ((4 * hf + kk) ^ ((c32 >> 1) & 7)));
     const uint32_t a_off = (uint32_t)(wm * 32 * 128), b_off = (uint32_t)((BM + wn * WTN) * 128);
-    const uint32_t sa_off = (uint32_t)(SC_OFF + 8 * (32 * wm + c32) + 4 * hf);
-    const uint32_t sb_off = (uint32_t)(SC_OFF + 8 * (BM + wn * WTN + c32) + 4 * hf);
+    const uint32_t sa_off = (uint32_t)(SC_OFF + 32 * (32 * wm + c32) + 4 * hf);
+    const uint32_t sb_off = (uint32_t)(SC_OFF + 32 * (BM + wn * WTN + c32) + 4 * hf);
+#pragma unroll
+    for (int ph = 0; ph < PHASES; ++ph) issue_scales(ph, 0);
     load_scales(0);
     store_scales(0);
     load_scales(min(1, nsteps - 1));
+    // (every step issues LOADS loads, so that the waits can count)
 #pragma unroll
-    for (int t = 0; t < NS; ++t)
+    for (int t = 0; t < NS; ++t) {
+        issue_scales(0, 1);
 #pragma unroll
-        for (int p = 0; p < LOADS; ++p) issue(p, t, t * STAGE);
+        for (int p = 0; p < CODES; ++p) issue(p, t, t * STAGE);
+    }
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (NS - 1)) & ~0xF00);
     __syncthreads();
     auto main_loop = [&](auto tmc) {
@@ -270,13 +284,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
             else
                 fb[buf][q - TA] = *reinterpret_cast<const u32x4*>(smem + (stage + off_k[kk] + b_off) + 4096 * (q - TA));
         };
-        auto read_scales = [&](uint32_t stage, uint32_t (&da)[TA], uint32_t (&db)[TN]) {
+        auto read_scales = [&](int kc, uint32_t (&xa)[TA], uint32_t (&xb)[TN]) {
+            const uint32_t at = (uint32_t)(((kc >> 2) & 1) * SC_HALF + 8 * (kc & 3));
+            // (blocks 4 .. 7 of a last step without them: zero, not the bytes
+            // after the row)
+            const uint32_t keep = kc + 1 == nsteps && 4 * hf >= tail ? 0u : ~0u;
 #pragma unroll
             for (int i = 0; i < TA; ++i)
-                da[i] = *reinterpret_cast<const uint32_t*>(smem + (stage + sa_off) + 256 * WM * i);
+                xa[i] = *reinterpret_cast<const uint32_t*>(smem + (at + sa_off) + 1024 * WM * i) & keep;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                db[j] = *reinterpret_cast<const uint32_t*>(smem + (stage + sb_off) + 256 * j);
+                xb[j] = *reinterpret_cast<const uint32_t*>(smem + (at + sb_off) + 1024 * j) & keep;
         };
         read_scales(0, sa, sb);
 #pragma unroll
@@ -289,25 +307,33 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
                 constexpr int kk = decltype(kkc)::value, buf = kk & 1;
                 if constexpr (kk == 3) {
                     __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (NS - 2)) & ~0xF00);
-                    store_scales(nxt);
+                    store_scales(s + 1);
                     __syncthreads();
-                    read_scales(nxt, na, nb);
+                    read_scales(s + 1, na, nb);
                     load_scales(min(s + 2, nsteps - 1));
                 }
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
                     __builtin_amdgcn_sched_barrier(0);
-                    constexpr int kR = (TA + TN + TN - 1) / TN, kL = (LOADS + TN - 1) / TN;
+                    constexpr int kR = (TA + TN + TN - 1) / TN;
 #pragma unroll
                     for (int q = j * kR; q < (j + 1) * kR && q < TA + TN; ++q)
                         read_frag(q, kk < 3 ? cur : nxt, (kk + 1) & 3, buf ^ 1);
 #pragma unroll
-                    for (int i = 0; i < TA; ++i)
+                    for (int i = 0; i < TA; ++i) {
                         acc[j][i] = mfma_kk<kk>(fb[buf][j], fa[buf][i], acc[j][i], sb[j], sa[i]);
-                    if constexpr (kk == 3) {
-                        __builtin_amdgcn_sched_barrier(0);
+                        // (a matrix instruction takes 32 cycles of its unit,
+                        // about what one load takes to issue)
+                        if constexpr (kk == 3) {
+                            constexpr int kM = TN * TA;
+                            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int p = j * kL; p < (j + 1) * kL && p < LOADS; ++p) issue(p, s + NS, cur);
+                            for (int p = (j * TA + i) * LOADS / kM; p < (j * TA + i + 1) * LOADS / kM; ++p) {
+                                if (p < CODES) issue(p, s + NS, cur);
+                                else issue_scales((s + 1) & 3, ((s + 1) >> 2) + 1);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);

@@ -185,11 +185,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
         const int64_t mt = id / nt;
         tn = (int)(id - mt * nt);
         if (mt >= g.tile_off[g.E]) return;
-        int lo = 0, hi = g.E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (g.tile_off[mid] <= mt) lo = mid; else hi = mid;
-        }
+        const int lo = group_of_tile(g.tile_off, g.E, (int)mt);
         expert = lo;
         row_beg = (int64_t)g.row_off[lo] + (mt - g.tile_off[lo]) * (16 * MB);
         row_end = min((int64_t)g.row_off[lo + 1], row_beg + 16 * MB);
