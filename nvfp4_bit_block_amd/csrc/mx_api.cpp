@@ -130,7 +130,7 @@ MxMoeLayout layout_mx_moe(const nvfp4_mx_moe_problem& p) {
     l.xs = off; off += packed_scales_bytes(p.T, p.H);
     l.hc = off; off += packed_codes_bytes(S, p.I);
     l.hs = off; off += packed_scales_bytes(S, p.I);
-    l.y = off; off += align_up((size_t)S * (size_t)p.H * 4);
+    l.y = off; off += align_up((size_t)S * (size_t)p.H * 2);
     l.total = off;
     return l;
 }
@@ -345,7 +345,7 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
     uint8_t* xs = at<uint8_t>(workspace, l.xs);
     uint8_t* hc = at<uint8_t>(workspace, l.hc);
     uint8_t* hs = at<uint8_t>(workspace, l.hs);
-    float* Y = at<float>(workspace, l.y);
+    uint16_t* Y = at<uint16_t>(workspace, l.y);
     int32_t st = api_hip(launch_moe_route(t->topk_ids, S, E, bm, row_off, tile_off, perm, inv,
                                           at<int32_t>(workspace, l.pos_group), at<int32_t>(workspace, l.route), s),
                          "mx_moe route");
@@ -359,12 +359,12 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
         up.perm = perm;
         up.row_off = down.row_off = row_off;
         up.tile_off = down.tile_off = tile_off;
-        down.yf = Y;
+        down.y = Y;
         st = api_hip(launch_mx_group_up(up, bm, grid_m, s), "mx_moe gate/up");
         if (st) return st;
         st = api_hip(launch_mx_group_down(down, bm, grid_m, s), "mx_moe down");
         if (st) return st;
-        return api_hip(launch_moe_combine(Y, inv, t->topk_weights, p->T, (int32_t)p->top_k, p->H, t->out, s),
+        return api_hip(launch_mx_combine(Y, inv, t->topk_weights, p->T, (int32_t)p->top_k, p->H, t->out, s),
                        "mx_moe combine");
     }
     MxGemmArgs g1;
@@ -400,9 +400,9 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
     g2.groups = E;
     g2.out = Y;
     g2.ldo = p->H;
-    st = api_hip(launch_mx_gemm(g2, MxEpi::kDown, grid_m, s), "mx_moe down");
+    st = api_hip(launch_mx_gemm(g2, MxEpi::kStoreBf16, grid_m, s), "mx_moe down");
     if (st) return st;
-    return api_hip(launch_moe_combine(Y, inv, t->topk_weights, p->T, (int32_t)p->top_k, p->H, t->out, s),
+    return api_hip(launch_mx_combine(Y, inv, t->topk_weights, p->T, (int32_t)p->top_k, p->H, t->out, s),
                    "mx_moe combine");
 }
 

@@ -37,10 +37,20 @@ __device__ __forceinline__ uint32_t mx_encode8(uint32_t w0, uint32_t w1, uint32_
     o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, w3), d, 3);
     return o;
 }
-// fp32 -> bf16 pattern, round to nearest even; a NaN (a block of scale byte
-// 255 makes them) stays one.
-__device__ __forceinline__ uint32_t f32_to_bf16(float f) {
-    return f != f ? 0x7FC0u : f32_to_bf16_rne(f);
+// Two fp32 -> two bf16 patterns in a word, round to nearest even (one
+// instruction; a NaN, which a block of scale byte 255 makes, stays one).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// silu(g) * u from the hardware's exponential and reciprocal: a few parts in
+// 2^22 for the gate values a layer meets, against the half step of 2^-9 that
+// rounding h to bf16 takes.  (With the library's exponential and a correctly
+// rounded division this took 200 of the 1000 us of the gate/up product at
+// 4096 tokens x 8 of 256 experts, 6144 x 2048.)
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g)) * u;
 }
 
 // The scale the encoder divides by: a block of byte 255 decodes as NaN

@@ -18,11 +18,12 @@
 // word and byte kk is selected by the instruction.
 //
 // Codes go from global memory straight into LDS (buffer_load ... lds, 1 KB =
-// 8 rows per instruction) through NS stages, one barrier per step.  LDS rows
+// 8 rows per instruction), one barrier per step: activations through two
+// stages, weights, which mostly come from farther away, through NS.  LDS rows
 // are not padded: row r keeps its 16-byte chunk c in slot c ^ ((r / 2) % 8),
 // so that 16 consecutive rows' fragment reads cover all banks.  A step's 8
 // scale bytes of a row would cost a request to L2 like the 128 bytes of its
-// codes; they come 32 at a time, for four steps, into a ring of their own.
+// codes; they come for RSTEP steps at a time into a ring of their own.
 // Blocks past K and rows past the operand load as zeros.
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
@@ -43,24 +44,28 @@ __device__ __forceinline__ f32x16 mfma_kk(u32x4 w, u32x4 a, f32x16 c, uint32_t s
 }
 
 // TM, TN: 32-row blocks of activations and of weights per wave; WM x WN
-// waves; NS stages.  The activation blocks are dealt to the wave rows in turn
-// (wave row wm has blocks wm, wm + WM, ..), and a tile of fewer rows runs a
-// main loop of as many blocks as its fullest wave has.  ALIGNED: K % 128 == 0,
+// waves; NS weight stages; scales for RSTEP steps at a time.  The activation
+// blocks are dealt to the wave rows in turn (wave row wm has blocks wm,
+// wm + WM, ..), and a tile of fewer rows runs a main loop of as many blocks
+// as its fullest wave has.  ALIGNED: K % 128 == 0,
 // so a row's scale bytes are whole words (else each step's are shifted into
 // place on their way through registers).
-template <int TM, int TN, int WM, int WN, int NS, MxEpi EP, bool ALIGNED>
+template <int TM, int TN, int WM, int WN, int NS, int RSTEP, MxEpi EP, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     constexpr int NW = WM * WN, NT = 64 * NW;
     constexpr int WTN = 32 * TN, BM = 32 * TM * WM, BN = WTN * WN;
-    constexpr int SLABS = (BM + BN) / 8, CODES = (SLABS + NW - 1) / NW;  // code slabs of 1 KB: activations, then weights
-    constexpr int STAGE = (BM + BN) * 128;
-    // scale ring: two halves, each four steps' 32 bytes of every row; slabs of
-    // 32 rows (1 KB), one per wave and phase
-    constexpr int SC_OFF = NS * STAGE, SC_HALF = (BM + BN) * 32;
-    constexpr int SC_SLABS = (BM + BN) / 32, PHASES = (SC_SLABS + NW - 1) / NW;
+    // code slabs of 1 KB, and how many of them a wave loads
+    constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW, CODES = CA + CB;
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "copy");
+    constexpr int A_STAGE = BM * 128, B_STAGE = BN * 128, B_OFF = 2 * A_STAGE;
+    // scale ring: two halves, each RSTEP steps' bytes of every row, in slabs
+    // of 1 KB, one per wave and phase
+    constexpr int SCB = 8 * RSTEP, SC_OFF = B_OFF + NS * B_STAGE, SC_HALF = (BM + BN) * SCB;
+    constexpr int SCR = 1024 / SCB, LPR = SCB / 16;  // rows of a slab, lanes of a row
+    constexpr int SC_SLABS = (BM + BN) / SCR, PHASES = (SC_SLABS + NW - 1) / NW;
     constexpr int SC_PER_T = (BM + BN + NT - 1) / NT;
-    constexpr int LOADS = CODES + (ALIGNED ? 1 : 0);  // of a wave, per step
-    static_assert(NS >= 2 && NS <= 3 && PHASES <= (NS == 2 ? 4 : 3) && LOADS * (NS - 1) <= 63, "stages");
+    static_assert((RSTEP == 2 || RSTEP == 4) && BM % SCR == 0 && BN % SCR == 0 && PHASES <= RSTEP, "scales");
+    static_assert(NS == 2 || NS == 3, "stages");
     constexpr int LDS = SC_OFF + 2 * SC_HALF;
     static_assert(LDS <= 160 * 1024, "LDS");
     constexpr bool kGateUp = EP == MxEpi::kGateUp;
@@ -135,60 +140,57 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     const u32x4 rb = make_rsrc(g.b_codes + ((int64_t)grp * g.N + n0) * KB,
                                (uint64_t)(kGateUp || brows < BN ? brows : BN) * KB);
 
-    // ---- copy assignments.  Code slab sl: tile rows 8 sl + lane / 8 (the
-    // activations', then the weights'), slot lane % 8.
+    // ---- copy assignments.  Code slab sl of an operand: its rows 8 sl +
+    // lane / 8, slot lane % 8.  Load p of a wave: CA slabs of activations,
+    // then CB of weights.
     auto tile_row = [&](int r) -> int64_t { return r < BM ? a_row(r) : r < BM + BN ? b_row(r - BM) : -1; };
+    auto slab = [&](int p) { return p < CA ? CA * wave + p : CB * wave + p - CA; };
     // the chunk in this lane's slot of slab sl
     auto chunk_of = [&](int sl) { return (lane & 7) ^ (((8 * sl + (lane >> 3)) >> 1) & 7); };
-    // (slabs beyond an even deal repeat the last one)
-    auto slab = [&](int u) { return SLABS % NW == 0 ? CODES * wave + u : min(CODES * wave + u, SLABS - 1); };
     uint32_t vc[CODES];
 #pragma unroll
-    for (int u = 0; u < CODES; ++u) {
-        const int sl = slab(u);
-        const int64_t src = tile_row(8 * sl + (lane >> 3));
-        vc[u] = src < 0 ? kOob : (uint32_t)src * KB + 16u * chunk_of(sl);
+    for (int p = 0; p < CODES; ++p) {
+        const int r = 8 * slab(p) + (lane >> 3);
+        const int64_t src = p < CA ? a_row(r) : b_row(r);
+        vc[p] = src < 0 ? kOob : (uint32_t)src * KB + 16u * chunk_of(slab(p));
     }
-    // scales.  ALIGNED: slab sl holds tile rows 32 sl + lane / 2, half lane % 2
-    // of their 32 bytes; in phase p a wave loads slab p NW + wave.  Otherwise
-    // thread t carries tile rows t, t + NT, .. of one step through registers,
+    // scales.  ALIGNED: slab sl holds tile rows SCR sl + lane / LPR (the
+    // activations', then the weights'), 16 bytes lane % LPR of theirs; in
+    // phase p a wave loads slab p NW + wave.  Otherwise thread t carries tile rows t, t + NT, .. of one step through registers,
     // from a base rounded down to a word.
     const uint8_t* const as = g.a_scales + a0 * KS;
     const uint8_t* const bs = g.b_scales + ((int64_t)grp * g.N + n0) * KS;
     const uint32_t da = ALIGNED ? 0u : (uint32_t)(uintptr_t)as & 3u, db = ALIGNED ? 0u : (uint32_t)(uintptr_t)bs & 3u;
     const u32x4 rsa = make_rsrc(as - da, ((uint64_t)(gather ? g.a_src_rows : row_end - row_beg) * KS + da + 3) & ~3ull);
     const u32x4 rsb = make_rsrc(bs - db, ((uint64_t)(kGateUp || brows < BN ? brows : BN) * KS + db + 3) & ~3ull);
+    auto sc_slab = [&](int ph) { return min(ph * NW + wave, SC_SLABS - 1); };  // (one too many repeats the last)
     uint32_t vs[ALIGNED ? PHASES : SC_PER_T];
     uint2 sv[ALIGNED ? 1 : SC_PER_T];
 #pragma unroll
     for (int u = 0; u < (ALIGNED ? PHASES : SC_PER_T); ++u) {
-        const int r = ALIGNED ? 32 * (u * NW + wave) + (lane >> 1) : tid + u * NT;
+        const int r = ALIGNED ? SCR * sc_slab(u) + lane / LPR : tid + u * NT;
         const int64_t src = tile_row(r);
-        vs[u] = src < 0 ? kOob : (uint32_t)src * KS + (ALIGNED ? 16u * (lane & 1) : r < BM ? da : db);
+        vs[u] = src < 0 ? kOob : (uint32_t)src * KS + (ALIGNED ? 16u * (lane % LPR) : r < BM ? da : db);
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
-    // Phase ph of the scales of steps 4 q .. 4 q + 3 (phases and slabs that do
-    // not exist repeat one that does).  The 32 bytes may run past the row,
-    // whose neighbour's bytes no step uses, and past the tensor, where the
+    // Phase ph of the scales of steps RSTEP q .. RSTEP (q + 1) - 1 (a
+    // phase too many repeats the last).  The bytes may run past
+    // the row, whose neighbour's bytes no step uses, and past the tensor, where the
     // range check, made word by word, gives zeros.
     auto issue_scales = [&](int ph, int q) {
         if constexpr (ALIGNED) {
             ph = min(ph, PHASES - 1);
-            int sl = ph * NW + wave;
+            const int sl = sc_slab(ph);
             uint32_t v = vs[0];
 #pragma unroll
             for (int u = 1; u < PHASES; ++u) v = ph == u ? vs[u] : v;
-            if (SC_SLABS % NW != 0 && sl >= SC_SLABS) {
-                sl = wave;
-                v = vs[0];
-            }
-            const bool isa = 32 * sl < BM;
+            const bool isa = SCR * sl < BM;
             u32x4 r = isa ? rsa : rsb;
             r.x = __builtin_amdgcn_readfirstlane(r.x);
             r.y = __builtin_amdgcn_readfirstlane(r.y);
             r.z = __builtin_amdgcn_readfirstlane(r.z);
             r.w = kRsrcWord3;
-            lds_load16(r, v + 32u * (uint32_t)q, 0u, lds0 + (uint32_t)(SC_OFF + (q & 1) * SC_HALF + 1024 * sl));
+            lds_load16(r, v + (uint32_t)(SCB * q), 0u, lds0 + (uint32_t)(SC_OFF + (q & 1) * SC_HALF + 1024 * sl));
         }
     };
     auto load_scales = [&](int kc) {
@@ -215,24 +217,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
             for (int u = 0; u < SC_PER_T; ++u) {
                 const int r = tid + u * NT;
                 if (r < BM + BN)
-                    *reinterpret_cast<uint2*>(smem + SC_OFF + ((kc >> 2) & 1) * SC_HALF + 32 * r + 8 * (kc & 3)) = sv[u];
+                    *reinterpret_cast<uint2*>(smem + SC_OFF + ((kc / RSTEP) & 1) * SC_HALF + SCB * r + 8 * (kc % RSTEP)) =
+                        sv[u];
             }
         }
     };
-    // Code load p (0 .. CODES - 1) of this wave for step kc into a stage.  In
-    // the last step the chunks past K are pushed out of range, and steps past
-    // the last load nothing: a resource of no bytes, at offset zero so that
-    // the range check holds whichever way it counts the offset.
-    auto issue = [&](int p, int kc, uint32_t stage) {
+    // Code load p (0 .. CODES - 1) of this wave for step kc, into the stage at
+    // `at`.  In the last step the chunks past K are pushed out of range, and
+    // steps past the last load nothing: a resource of no bytes, at offset zero
+    // so that the range check holds whichever way it counts the offset.
+    auto issue = [&](int p, int kc, uint32_t at) {
         const bool live = kc < nsteps, last = kc + 1 == nsteps;
-        const int sl = slab(p);
-        u32x4 r = 8 * sl < BM ? ra : rb;
-        r.x = __builtin_amdgcn_readfirstlane(r.x);
-        r.y = __builtin_amdgcn_readfirstlane(r.y);
+        u32x4 r = p < CA ? ra : rb;
         r.z = __builtin_amdgcn_readfirstlane(live ? r.z : 0u);
-        r.w = kRsrcWord3;
-        const uint32_t cut = last && chunk_of(sl) >= tail ? kOob : 0u;
-        lds_load16(r, vc[p] | cut, live ? (uint32_t)kc * 128u : 0u, lds0 + stage + (uint32_t)(sl * 1024));
+        const uint32_t cut = last && chunk_of(slab(p)) >= tail ? kOob : 0u;
+        lds_load16(r, vc[p] | cut, live ? (uint32_t)kc * 128u : 0u, lds0 + at + (uint32_t)(slab(p) * 1024));
     };
 
     f32x16 acc[TN][TM];
@@ -257,56 +256,65 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     uint32_t off_k[4];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) off_k[kk] = (uint32_t)(c32 * 128 + 16 * ((4 * hf + kk) ^ ((c32 >> 1) & 7)));
-    const uint32_t a_off = (uint32_t)(wm * 32 * 128), b_off = (uint32_t)((BM + wn * WTN) * 128);
-    const uint32_t sa_off = (uint32_t)(SC_OFF + 32 * (32 * wm + c32) + 4 * hf);
-    const uint32_t sb_off = (uint32_t)(SC_OFF + 32 * (BM + wn * WTN + c32) + 4 * hf);
+    const uint32_t a_off = (uint32_t)(wm * 32 * 128), b_off = (uint32_t)(wn * WTN * 128);
+    const uint32_t sa_off = (uint32_t)(SC_OFF + SCB * (32 * wm + c32) + 4 * hf);
+    const uint32_t sb_off = (uint32_t)(SC_OFF + SCB * (BM + wn * WTN + c32) + 4 * hf);
 #pragma unroll
     for (int ph = 0; ph < PHASES; ++ph) issue_scales(ph, 0);
     load_scales(0);
     store_scales(0);
     load_scales(min(1, nsteps - 1));
-    // (every step issues LOADS loads, so that the waits can count)
+    // In the order that the waits count on: a step's scales and activations
+    // before its weights, and with NS = 3 the weights of a step further on.
 #pragma unroll
-    for (int t = 0; t < NS; ++t) {
-        issue_scales(0, 1);
+    for (int p = CA; p < CODES; ++p) issue(p, 0, B_OFF);
+    if constexpr (NS == 3)
 #pragma unroll
-        for (int p = 0; p < CODES; ++p) issue(p, t, t * STAGE);
-    }
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (NS - 1)) & ~0xF00);
+        for (int p = CA; p < CODES; ++p) issue(p, 1, B_OFF + B_STAGE);
+#pragma unroll
+    for (int p = 0; p < CA; ++p) issue(p, 0, 0);
+    issue_scales(0, 1);
+#pragma unroll
+    for (int p = 0; p < CODES; ++p)
+        issue(p, p < CA ? 1 : NS - 1, p < CA ? (uint32_t)A_STAGE : (uint32_t)(B_OFF + (NS - 1) * B_STAGE));
+    // (step 0: everything before that last set, whose activations are step 1's)
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(CODES + (ALIGNED ? 1 : 0)) & ~0xF00);
     __syncthreads();
     auto main_loop = [&](auto tmc) {
         constexpr int TA = decltype(tmc)::value;  // activation blocks in use
         u32x4 fa[2][TA], fb[2][TN];
         uint32_t sa[TA], sb[TN];
-        auto read_frag = [&](int q, uint32_t stage, int kk, int buf) {  // q: 0 .. TA + TN - 1
+        // fragment q (TA activations, then TN weights) of the stages at sta, stb
+        auto read_frag = [&](int q, uint32_t sta, uint32_t stb, int kk, int buf) {
             if (q < TA)
-                fa[buf][q] = *reinterpret_cast<const u32x4*>(smem + (stage + off_k[kk] + a_off) + 4096 * WM * q);
+                fa[buf][q] = *reinterpret_cast<const u32x4*>(smem + (sta + off_k[kk] + a_off) + 4096 * WM * q);
             else
-                fb[buf][q - TA] = *reinterpret_cast<const u32x4*>(smem + (stage + off_k[kk] + b_off) + 4096 * (q - TA));
+                fb[buf][q - TA] = *reinterpret_cast<const u32x4*>(smem + (stb + off_k[kk] + b_off) + 4096 * (q - TA));
         };
         auto read_scales = [&](int kc, uint32_t (&xa)[TA], uint32_t (&xb)[TN]) {
-            const uint32_t at = (uint32_t)(((kc >> 2) & 1) * SC_HALF + 8 * (kc & 3));
+            const uint32_t at = (uint32_t)(((kc / RSTEP) & 1) * SC_HALF + 8 * (kc % RSTEP));
             // (blocks 4 .. 7 of a last step without them: zero, not the bytes
             // after the row)
             const uint32_t keep = kc + 1 == nsteps && 4 * hf >= tail ? 0u : ~0u;
 #pragma unroll
             for (int i = 0; i < TA; ++i)
-                xa[i] = *reinterpret_cast<const uint32_t*>(smem + (at + sa_off) + 1024 * WM * i) & keep;
+                xa[i] = *reinterpret_cast<const uint32_t*>(smem + (at + sa_off) + 32 * SCB * WM * i) & keep;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                xb[j] = *reinterpret_cast<const uint32_t*>(smem + (at + sb_off) + 1024 * j) & keep;
+                xb[j] = *reinterpret_cast<const uint32_t*>(smem + (at + sb_off) + 32 * SCB * j) & keep;
         };
         read_scales(0, sa, sb);
 #pragma unroll
-        for (int q = 0; q < TA + TN; ++q) read_frag(q, 0, 0, 0);
-        uint32_t cur = 0;
+        for (int q = 0; q < TA + TN; ++q) read_frag(q, 0, B_OFF, 0, 0);
+        uint32_t ca = 0, cb = B_OFF;  // this step's stages
         for (int s = 0; s < nsteps; ++s) {
-            const uint32_t nxt = cur + STAGE == NS * STAGE ? 0 : cur + STAGE;
+            const uint32_t xa = A_STAGE - ca, xb = cb + B_STAGE == SC_OFF ? B_OFF : cb + B_STAGE;  // the next one's
             uint32_t na[TA], nb[TN];
             auto group = [&](auto kkc) {
                 constexpr int kk = decltype(kkc)::value, buf = kk & 1;
                 if constexpr (kk == 3) {
-                    __builtin_amdgcn_s_waitcnt(vmcnt_imm(LOADS * (NS - 2)) & ~0xF00);
+                    // (NS = 3: the weights issued last, a step ahead, may be out)
+                    __builtin_amdgcn_s_waitcnt(vmcnt_imm(NS == 3 ? CB : 0) & ~0xF00);
                     store_scales(s + 1);
                     __syncthreads();
                     read_scales(s + 1, na, nb);
@@ -318,19 +326,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
                     constexpr int kR = (TA + TN + TN - 1) / TN;
 #pragma unroll
                     for (int q = j * kR; q < (j + 1) * kR && q < TA + TN; ++q)
-                        read_frag(q, kk < 3 ? cur : nxt, (kk + 1) & 3, buf ^ 1);
+                        read_frag(q, kk < 3 ? ca : xa, kk < 3 ? cb : xb, (kk + 1) & 3, buf ^ 1);
 #pragma unroll
                     for (int i = 0; i < TA; ++i) {
                         acc[j][i] = mfma_kk<kk>(fb[buf][j], fa[buf][i], acc[j][i], sb[j], sa[i]);
                         // (a matrix instruction takes 32 cycles of its unit,
                         // about what one load takes to issue)
                         if constexpr (kk == 3) {
-                            constexpr int kM = TN * TA;
+                            constexpr int kM = TN * TA, kL = CODES + 1;
                             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                            for (int p = (j * TA + i) * LOADS / kM; p < (j * TA + i + 1) * LOADS / kM; ++p) {
-                                if (p < CODES) issue(p, s + NS, cur);
-                                else issue_scales((s + 1) & 3, ((s + 1) >> 2) + 1);
+                            for (int p = (j * TA + i) * kL / kM; p < (j * TA + i + 1) * kL / kM; ++p) {
+                                if (p == 0) issue_scales((s + 1) % RSTEP, (s + 1) / RSTEP + 1);
+                                else if (p <= CA) issue(p - 1, s + 2, ca);
+                                else issue(p - 1, s + NS, cb);
                             }
                             __builtin_amdgcn_sched_barrier(0);
                         }
@@ -346,7 +355,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
             for (int i = 0; i < TA; ++i) sa[i] = na[i];
 #pragma unroll
             for (int j = 0; j < TN; ++j) sb[j] = nb[j];
-            cur = nxt;
+            ca = xa;
+            cb = xb;
         }
     };
     // blocks of the fullest wave row
@@ -364,6 +374,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     // of the wave, activation row 32 (i WM + wm) + c32.
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
+        if (i >= used) break;
         const int64_t row = row_beg + 32 * (i * WM + wm) + c32;
         if constexpr (kGateUp) {
             // (rows past the end take part in the exchange and store nothing)
@@ -373,14 +384,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
                 uint32_t w[8], m = 0;
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
-                    uint32_t pair = 0;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float gv = acc[j][i][2 * p + b], uv = acc[j + TN / 2][i][2 * p + b];
-                        pair |= f32_to_bf16(gv / (1.0f + expf(-gv)) * uv) << (16 * b);
-                    }
-                    w[p] = pair;
-                    m = max_bf16x2(m, pair);
+                    w[p] = pack_bf16(silu_mul(acc[j][i][2 * p], acc[j + TN / 2][i][2 * p]),
+                                     silu_mul(acc[j][i][2 * p + 1], acc[j + TN / 2][i][2 * p + 1]));
+                    m = max_bf16x2(m, w[p]);
                 }
                 m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
                 const uint32_t s = mx_scale_byte(m);
@@ -396,32 +402,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
                     if (hf == 0) g.out_scales[row * (g.ldo / 32) + hc / 32] = (uint8_t)s;
                 }
             }
-        } else if constexpr (EP == MxEpi::kDown) {
-            if (row >= row_end) continue;
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    // (N is the hidden size, a multiple of 32)
-                    const int64_t col = n0 + wn * WTN + 32 * j + 8 * p + 4 * hf;
-                    if (col < nlim)
-                        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(g.out) + row * g.ldo + col) =
-                            f32x4{acc[j][i][4 * p], acc[j][i][4 * p + 1], acc[j][i][4 * p + 2], acc[j][i][4 * p + 3]};
-                }
         } else {
             // a 32-row slab of the wave's tile meets in LDS and leaves as
             // 16-byte pieces of rows (pitch: 16 rows' 8-byte writes fall on
             // different banks)
             constexpr int kPitch = WTN * 2 + 16;
-            static_assert(NW * 32 * kPitch <= NS * STAGE, "epilogue slabs");
+            static_assert(NW * 32 * kPitch <= SC_OFF, "epilogue slabs");
             uint8_t* const slab = smem + wave * 32 * kPitch;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
                     *reinterpret_cast<uint2*>(slab + c32 * kPitch + 2 * (32 * j + 8 * p + 4 * hf)) =
-                        make_uint2(f32_to_bf16(acc[j][i][4 * p]) | (f32_to_bf16(acc[j][i][4 * p + 1]) << 16),
-                                   f32_to_bf16(acc[j][i][4 * p + 2]) | (f32_to_bf16(acc[j][i][4 * p + 3]) << 16));
+                        make_uint2(pack_bf16(acc[j][i][4 * p], acc[j][i][4 * p + 1]),
+                                   pack_bf16(acc[j][i][4 * p + 2], acc[j][i][4 * p + 3]));
             __builtin_amdgcn_wave_barrier();
             const int64_t row0 = row_beg + 32 * (i * WM + wm);
             const bool vec = (g.ldo & 7) == 0;
@@ -446,7 +440,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     }
 }
 
-template <int TM, int TN, int WM, int WN, int NS, MxEpi EP>
+// ONLY_ALIGNED: built for K % 128 == 0 alone.
+template <int TM, int TN, int WM, int WN, int NS, int RSTEP, MxEpi EP, bool ONLY_ALIGNED = false>
 hipError_t launch_cfg(const MxGemmArgs& g0, int grid_m, hipStream_t stream) {
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
     MxGemmArgs g = g0;
@@ -456,21 +451,40 @@ hipError_t launch_cfg(const MxGemmArgs& g0, int grid_m, hipStream_t stream) {
     int64_t wgs = mt * g.ntiles;
     if (g.groups > 0) wgs = (wgs + 7) / 8 * 8;  // a multiple of 8 for the XCD renumbering
     if (wgs < 1 || wgs >= ((int64_t)1 << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
-    if (g.K % 128 == 0)
-        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, NS, EP, true>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
+    if (ONLY_ALIGNED && g.K % 128 != 0) return hipErrorInvalidValue;
+    if (ONLY_ALIGNED || g.K % 128 == 0)
+        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, NS, RSTEP, EP, true>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
     else
-        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, NS, EP, false>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
+        hipLaunchKernelGGL((k_mx_gemm<TM, TN, WM, WN, NS, RSTEP, EP, ONLY_ALIGNED>), dim3((unsigned)wgs), dim3(64 * WM * WN), 0, stream, g);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Tiles, measured on MI355X with random codes (TFLOP/s; N x K 6144 x 16384 at
+// M = 4096 and 1024, 16384 x 2048 at M = 4096):
+//                      256 x 192   256 x 256   128 x 128 (two workgroups a CU)
+//   4096 x 6144 x 16384     3836        3545        3547
+//   1024 x 6144 x 16384     2276        2100        3066
+//   4096 x 16384 x 2048     2172        3000        2668
+// The large tiles need one workgroup per CU and few partly filled rounds; on
+// short rows 256 x 192's odd tile count and longer tail lose.
 hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream) {
-    switch (epi) {
-        case MxEpi::kStoreBf16: return launch_cfg<2, 2, 2, 2, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
-        case MxEpi::kGateUp: return launch_cfg<2, 2, 2, 2, 2, MxEpi::kGateUp>(g, grid_m, stream);
-        default: return launch_cfg<2, 2, 2, 2, 2, MxEpi::kDown>(g, grid_m, stream);
-    }
+    if (g.groups > 0)
+        return epi == MxEpi::kGateUp ? launch_cfg<3, 4, 2, 2, 3, 2, MxEpi::kGateUp>(g, grid_m, stream)
+                                     : launch_cfg<3, 4, 2, 2, 3, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
+    // share of the CUs' time that a tile's rounds fill
+    auto fill = [&](int64_t bm, int64_t bn, int64_t slots) {
+        const int64_t t = ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn);
+        return (double)t / (double)((t + slots - 1) / slots * slots) * (double)(g.M * g.N) /
+               (double)(t * bm * bn);
+    };
+    // (256 x 256 leaves no registers for the scales of an unaligned K)
+    const double f192 = fill(256, 192, 256) * (g.K >= 8192 ? 1.05 : 0.8), f256 = g.K % 128 ? 0.0 : fill(256, 256, 256);
+    const double f128 = fill(128, 128, 512) * 0.9;
+    if (f192 > f256 && f192 > f128) return launch_cfg<4, 3, 2, 2, 3, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
+    if (f256 > f128) return launch_cfg<2, 4, 4, 2, 2, 4, MxEpi::kStoreBf16, true>(g, grid_m, stream);
+    return launch_cfg<2, 2, 2, 2, 2, 4, MxEpi::kStoreBf16>(g, grid_m, stream);
 }
 
 }  // namespace nvfp4

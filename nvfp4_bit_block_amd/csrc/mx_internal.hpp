@@ -24,7 +24,6 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 enum class MxEpi : int {
     kStoreBf16 = 0,  // y = bf16(acc)
     kGateUp = 1,     // h = bf16(silu(g) * u), stored as MXFP4
-    kDown = 2,       // Y = acc (fp32)
 };
 
 struct MxGemmArgs {
@@ -42,13 +41,13 @@ struct MxGemmArgs {
     const int32_t* tile_off = nullptr;
     int32_t groups = 0;
     int32_t ntiles = 0;                 // set by the launcher
-    void* out = nullptr;                // kStoreBf16: bf16 [M, ldo]; kDown: fp32 [M, ldo]; kGateUp: codes [M, ldo/2]
+    void* out = nullptr;                // kStoreBf16: bf16 [M, ldo]; kGateUp: codes [M, ldo/2]
     uint8_t* out_scales = nullptr;      // kGateUp: [M, ldo/32]
     int64_t ldo = 0;
 };
 
 // Row tile of the grouped launches.
-constexpr int kMxMoeBM = 128;
+constexpr int kMxMoeBM = 192;
 // grid_m bounds the row tiles of a grouped launch (ungrouped: ignored).
 hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream);
 
@@ -67,7 +66,6 @@ struct MxStreamArgs {
     const int32_t* row_off = nullptr;   // row and tile offsets as in MxGemmArgs
     const int32_t* tile_off = nullptr;
     uint16_t* y = nullptr;              // bf16 outputs
-    float* yf = nullptr;                // kGroupDown: fp32 [S, N]
     uint8_t* h_codes = nullptr;         // gate/up forms: MXFP4 h [S, N/4], [S, N/64]
     uint8_t* h_scales = nullptr;
     int32_t ntiles = 0, slice = 0;      // set by the launcher
@@ -83,6 +81,11 @@ hipError_t launch_mx_slot_down(const MxStreamArgs& g, int64_t tokens, hipStream_
 // bm (16 or 32): rows of one workgroup; mtiles bounds the row tiles.
 hipError_t launch_mx_group_up(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
 hipError_t launch_mx_group_down(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
+
+// out[t] = bf16(sum_j w[t, j] * Y[inv[t * top_k + j]]) over expert-sorted bf16
+// rows Y [S, H], slots in order, inv < 0 skipped; H % 32 == 0.
+hipError_t launch_mx_combine(const uint16_t* Y, const int32_t* inv, const float* w, int64_t T, int32_t top_k, int64_t H,
+                             uint16_t* out, hipStream_t stream);
 
 // -------------------------------------------------------------------- gate --
 

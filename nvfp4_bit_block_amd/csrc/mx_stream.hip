@@ -292,13 +292,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
             const int m = p >> 3, q = p & 7;
             const int ln = 16 * (q & 3) + (m & 15), tile = q >> 2;
             const f32x4 gv = total(tile * MB + (m >> 4), ln), uv = total((2 + tile) * MB + (m >> 4), ln);
-            uint32_t w[2] = {0, 0}, mx = 0;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t h = f32_to_bf16(gv[r] / (1.0f + expf(-gv[r])) * uv[r]);
-                w[r >> 1] |= h << (16 * (r & 1));
-            }
-            mx = max_bf16x2(max_bf16x2(0, w[0]), w[1]);
+            const uint32_t w[2] = {pack_bf16(silu_mul(gv[0], uv[0]), silu_mul(gv[1], uv[1])),
+                                   pack_bf16(silu_mul(gv[2], uv[2]), silu_mul(gv[3], uv[3]))};
+            uint32_t mx = max_bf16x2(max_bf16x2(0, w[0]), w[1]);
             mx = max(mx, dpp_u32<0xB1>(mx));
             mx = max(mx, dpp_u32<0x4E>(mx));
             mx = max(mx, dpp_u32<0x141>(mx));  // the 8 lanes of a row
@@ -317,12 +313,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
             const int64_t col = n0 + 16 * (t / MB) + 4 * (ln >> 4);
             if (row >= row_end || col >= g.N) continue;
             const f32x4 v = total(t, ln);
-            if constexpr (MODE == Mode::kGroupDown) {
-                *reinterpret_cast<f32x4*>(g.yf + row * g.N + col) = v;  // (N is a multiple of 32)
-            } else {
+            {
                 uint16_t* const dst = g.y + row * g.N + col;
-                const uint32_t lo = f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16);
-                const uint32_t hi = f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16);
+                const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
                 if ((g.N & 3) == 0) {
                     *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
                 } else {

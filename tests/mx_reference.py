@@ -62,12 +62,13 @@ def product(a, w):
 
 
 def experts(x_bits, ids, tw, w13, w2):
-    """The routed-expert layer; returns (out, magnitude): `magnitude` sums the
-    absolute values of the slots' products, for error bounds."""
+    """The routed-expert layer; returns (out, magnitude, slots) with, for error
+    bounds, the sums of the absolute values of the slots' products and of
+    their weighted results."""
     T, H = x_bits.shape
     I = w2[0].shape[-1] * 2
     xh = mx_decode(*mx_encode(x_bits))
-    out, mag = np.zeros((T, H)), np.zeros((T, H))
+    out, mag, slots = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
     E = w13[0].shape[0]
     for e in range(E):
         t, j = np.nonzero(ids == e)
@@ -77,9 +78,11 @@ def experts(x_bits, ids, tw, w13, w2):
         g, u = gu[:, :I], gu[:, I:]
         h = mx_decode(*mx_encode(bf16_round(g / (1.0 + np.exp(-g)) * u)))
         w = mx_decode(w2[0][e], w2[1][e])
-        np.add.at(out, t, (h @ w.T) * tw[t, j, None])
+        y = (h @ w.T) * tw[t, j, None]
+        np.add.at(out, t, y)
+        np.add.at(slots, t, np.abs(y))
         np.add.at(mag, t, (np.abs(h) @ np.abs(w).T) * np.abs(tw[t, j, None]))
-    return out, mag
+    return out, mag, slots
 
 
 # ------------------------------------------------------------------- gate --

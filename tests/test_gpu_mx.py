@@ -5,6 +5,8 @@ Quantize and dequantize: bit for bit.  Products: the codes' products are exact
 and are summed in fp32 in some order, so the sum is off by at most
 K * 2^-23 of the sum of magnitudes (2^-23 rather than a half step: the matrix
 units may truncate), then one rounding to bf16, 2^-8 relative.  The layer
+rounds each slot's result to bf16 when it sorts the slots by expert (at most
+2^-8 of the slot's result, so 2^-8 of the sum of their magnitudes) and
 adds the rounding of h to bf16 and to MXFP4, which the definition has too: an
 h that lies closer to a border than the error of its sum may take the
 neighbouring code, so the layer's inputs here give sums that fp32 holds
@@ -149,12 +151,12 @@ def _run_experts(x, ids, tw, w13, w2, **kw):
 
 
 def _check_experts(y, x, ids, tw, w13, w2):
-    want, mag = ref.experts(x, ids, tw, w13, w2)
+    want, mag, slots = ref.experts(x, ids, tw, w13, w2)
     I = w2[0].shape[-1] * 2
     y = host_bf16_f32(y).astype(np.float64)
     assert np.isfinite(y).all()
     err = np.abs(y - want)
-    tight = I * 2.0 ** -23 * mag + 2.0 ** -8 * np.abs(want) + ids.shape[1] * 2.0 ** -8 * mag / np.sqrt(I)
+    tight = I * 2.0 ** -23 * mag + 2.0 ** -8 * (1 + 2.0 ** -8) * (np.abs(want) + slots) + ids.shape[1] * 2.0 ** -8 * mag / np.sqrt(I)
     rows = (err > tight).any(axis=1)
     assert rows.mean() <= 0.01 or rows.sum() <= 1, (rows.sum(), (err / tight).max())
     assert (err <= tight + mag / 8).all()
