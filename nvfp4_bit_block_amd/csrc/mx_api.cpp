@@ -104,7 +104,7 @@ struct MxMoeLayout {
 enum class MoePlan { kSlots, kStream16, kStream32, kTiles };
 MoePlan plan_mx_moe(const nvfp4_mx_moe_problem& p) {
     const int64_t S = p.T * p.top_k;
-    if (S <= 64 && p.H <= ((int64_t)1 << 20)) return MoePlan::kSlots;
+    if (S <= 64 && mx_slots_fit(p.H)) return MoePlan::kSlots;
     if (S <= 8 * p.E) return MoePlan::kStream16;
     if (S <= 20 * p.E) return MoePlan::kStream32;
     return MoePlan::kTiles;

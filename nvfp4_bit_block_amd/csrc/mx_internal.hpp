@@ -71,10 +71,10 @@ struct MxStreamArgs {
     int32_t ntiles = 0, slice = 0;      // set by the launcher
 };
 constexpr int kMxStreamMost = 64;       // activation rows of the plain form
-// Blocks of one row that a wave of the stream kernel quantizes at most, and
-// whether the plain form takes bf16 activations of this size.
-int mx_stream_slice(int64_t K);
+// Whether the plain form takes bf16 activations of this size, and the slot
+// forms tokens of this width (they quantize them into LDS).
 bool mx_stream_quantizes(int64_t M, int64_t K);
+bool mx_slots_fit(int64_t H);
 hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream);
 hipError_t launch_mx_slot_up(const MxStreamArgs& g, int64_t slots, hipStream_t stream);
 hipError_t launch_mx_slot_down(const MxStreamArgs& g, int64_t tokens, hipStream_t stream);

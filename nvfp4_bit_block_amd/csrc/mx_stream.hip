@@ -5,10 +5,10 @@
 // v_mfma_scale_f32_16x16x128_f8f6f4, weights as the A operand (16 weight
 // rows), activations as the B operand (16 rows, fewer are padded with copies
 // that are never stored).  A workgroup owns NR tiles of 16 weight rows; its
-// waves split K and their sums meet in LDS.  In a K unit of 256 elements lane
-// group g = lane / 16 takes blocks g and 4 + g, so an instruction reads 64
-// contiguous code bytes of each row; the unit's 8 scale bytes of a row are
-// one load, and the lane shifts its byte down.
+// waves split K and their sums meet in LDS.  In a step of 128 elements lane
+// group g = lane / 16 takes block g, so an instruction reads 64 contiguous
+// code bytes of each row; the scale bytes of a row are loaded for two or four
+// steps at once, and the lane shifts its byte down.
 //
 // Forms (Mode):
 //   kPlain     y = bf16(A W^T).
@@ -30,8 +30,12 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
+// Waves of a workgroup: eight, or four where a wave has four weight tiles and
+// more than 128 registers, so that several workgroups share a CU (one loads
+// while another adds up).
+constexpr int waves_of(int nr) { return nr == 4 ? 4 : 8; }
+// Waves per SIMD that the registers allow.
+constexpr int wpe_of(int nr, int mb) { return nr * mb <= 2 ? 4 : nr * mb <= 4 ? 2 : 1; }
 
 // One operand's rows as a lane sees them: the lane's row offset (bytes) into
 // codes and scales, from uniform bases.
@@ -46,26 +50,35 @@ struct Step {
     uint32_t s;
 };
 
-// FAST: K % 256 == 0 (whole units, 8-byte scale loads); otherwise units of
-// one 128-element step, scale bytes loaded one by one and blocks past K read
-// as zeros.
-template <bool FAST>
+// A unit of K: USTEPS steps of 128 elements whose scale bytes of a row are
+// one aligned load (4: 16 bytes, 2: 8 bytes); 1: K is no multiple of 256, the
+// scale bytes are loaded one by one and blocks past K read as zeros.
+template <int USTEPS>
 struct Unit {
-    static constexpr int kSteps = FAST ? 2 : 1;
-    Step st[kSteps];
+    Step st[USTEPS];
 };
 
-template <bool FAST, bool NT>
-__device__ __forceinline__ Unit<FAST> load_unit(const RowPtr& r, int unit, int g, int nblk) {
-    Unit<FAST> u;
-    if constexpr (FAST) {
-        const uint8_t* c = r.codes + (size_t)unit * 128 + 16 * g;
-        u.st[0].c = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c)) : *reinterpret_cast<const u32x4*>(c);
-        u.st[1].c = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c + 64))
-                       : *reinterpret_cast<const u32x4*>(c + 64);
-        const uint2 s = *reinterpret_cast<const uint2*>(r.scales + (size_t)unit * 8);
-        u.st[0].s = s.x >> (8 * g);
-        u.st[1].s = s.y >> (8 * g);
+template <int USTEPS, bool NT>
+__device__ __forceinline__ Unit<USTEPS> load_unit(const RowPtr& r, int unit, int g, int nblk) {
+    Unit<USTEPS> u;
+    if constexpr (USTEPS > 1) {
+        const uint8_t* c = r.codes + (size_t)unit * (64 * USTEPS) + 16 * g;
+#pragma unroll
+        for (int i = 0; i < USTEPS; ++i)
+            u.st[i].c = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c + 64 * i))
+                           : *reinterpret_cast<const u32x4*>(c + 64 * i);
+        uint32_t s[4];
+        if constexpr (USTEPS == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(r.scales + (size_t)unit * 16);
+            s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(r.scales + (size_t)unit * 8);
+            s[0] = v.x, s[1] = v.y;
+        }
+        // (this lane's byte is shifted down where it is used, so that the
+        // load need not be waited for here)
+#pragma unroll
+        for (int i = 0; i < USTEPS; ++i) u.st[i].s = s[i];
     } else {
         const int b = 4 * unit + g;
         u.st[0].c = u32x4{0, 0, 0, 0};
@@ -105,55 +118,75 @@ __device__ __forceinline__ void quantize_slice(const uint16_t* x, int b0, int bl
     }
 }
 
-enum class Mode : int { kPlain = 0, kSlotUp = 1, kSlotDown = 2, kGroupUp = 3, kGroupDown = 4 };
+// The weights (and packed activations) of UC units in flight.
+template <int NR, int MB, int USTEPS, int UC, bool A_LDS>
+struct Stream {
+    Unit<USTEPS> w[2][UC][NR];
+    Unit<USTEPS> a[A_LDS ? 1 : 2][A_LDS ? 1 : UC][A_LDS ? 1 : MB];
 
-// acc += W A^T over units [u0, u1) of one activation operand.
-template <int NR, int MB, bool FAST, int UC>
-__device__ __forceinline__ void run_units(f32x4 (&acc)[NR][MB], const RowPtr (&w)[NR], const RowPtr (&a)[MB], int u0,
-                                          int u1, int g, int nblk) {
-    Unit<FAST> wb[2][UC][NR];
-    auto fetch = [&](int u, int buf) {
+    __device__ __forceinline__ void fetch(const RowPtr (&wp)[NR], const RowPtr (&ap)[MB], int u, int u1, int buf, int g,
+                                          int nblk) {
 #pragma unroll
         for (int c = 0; c < UC; ++c)
-            if (u + c < u1)
+            if (u + c < u1) {
 #pragma unroll
-                for (int i = 0; i < NR; ++i) wb[buf][c][i] = load_unit<FAST, true>(w[i], u + c, g, nblk);
-    };
-    auto use = [&](int u, int buf) {
+                for (int i = 0; i < NR; ++i) w[buf][c][i] = load_unit<USTEPS, true>(wp[i], u + c, g, nblk);
+                if constexpr (!A_LDS)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) a[buf][c][m] = load_unit<USTEPS, false>(ap[m], u + c, g, nblk);
+            }
+    }
+    __device__ __forceinline__ void use(f32x4 (&acc)[NR][MB], const RowPtr (&ap)[MB], int u, int u1, int buf, int g,
+                                        int nblk) {
+        const int sh = USTEPS > 1 ? 8 * g : 0;
 #pragma unroll
         for (int c = 0; c < UC; ++c) {
             if (u + c >= u1) break;
-            Unit<FAST> ab[MB];
+            Unit<USTEPS> av[MB];
 #pragma unroll
-            for (int m = 0; m < MB; ++m) ab[m] = load_unit<FAST, false>(a[m], u + c, g, nblk);
+            for (int m = 0; m < MB; ++m) {
+                if constexpr (A_LDS) av[m] = load_unit<USTEPS, false>(ap[m], u + c, g, nblk);
+                else av[m] = a[buf][c][m];
+            }
 #pragma unroll
-            for (int s = 0; s < Unit<FAST>::kSteps; ++s)
+            for (int s = 0; s < USTEPS; ++s)
 #pragma unroll
                 for (int i = 0; i < NR; ++i)
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
-                        acc[i][m] = mx_mfma16<0, 0>(wb[buf][c][i].st[s].c, ab[m].st[s].c, acc[i][m],
-                                                    wb[buf][c][i].st[s].s, ab[m].st[s].s);
+                        acc[i][m] = mx_mfma16<0, 0>(w[buf][c][i].st[s].c, av[m].st[s].c, acc[i][m],
+                                                    w[buf][c][i].st[s].s >> sh, av[m].st[s].s >> sh);
         }
-    };
-    if (u0 >= u1) return;
-    fetch(u0, 0);
-    for (int u = u0; u < u1; u += 2 * UC) {
-        fetch(u + UC, 1);
-        use(u, 0);
-        fetch(u + 2 * UC, 0);
-        use(u + UC, 1);
     }
-}
+    // acc += W A^T over units [u0, u1), the first 2 UC of which are in flight
+    __device__ __forceinline__ void run(f32x4 (&acc)[NR][MB], const RowPtr (&wp)[NR], const RowPtr (&ap)[MB], int u0,
+                                        int u1, int g, int nblk) {
+        for (int u = u0; u < u1; u += 2 * UC) {
+            use(acc, ap, u, u1, 0, g, nblk);
+            fetch(wp, ap, u + 2 * UC, u1, 0, g, nblk);
+            use(acc, ap, u + UC, u1, 1, g, nblk);
+            fetch(wp, ap, u + 3 * UC, u1, 1, g, nblk);
+        }
+    }
+};
+
+enum class Mode : int { kPlain = 0, kSlotUp = 1, kSlotDown = 2, kGroupUp = 3, kGroupDown = 4 };
 
 // QUANT: the activation is bf16 and each wave quantizes its K slice into
 // LDS (kPlain: up to 16 rows; kSlotUp).  The LDS of a wave: `slice` blocks
 // per row.
-template <int NR, int MB, bool FAST, Mode MODE, bool QUANT>
-__global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
+template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT>
+__global__ __launch_bounds__(64 * waves_of(NR)) __attribute__((amdgpu_waves_per_eu(wpe_of(NR, MB))))
+void k_mx_stream(MxStreamArgs g) {
+    constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
     constexpr bool kUp = MODE == Mode::kSlotUp || MODE == Mode::kGroupUp;
     static_assert(!kUp || NR == 4, "gate/up: two tiles each");
-    constexpr int UC = NR * MB >= 4 ? 1 : NR >= 2 ? 2 : 4;
+    // units in flight, twice: 8 code loads a lane of weights alone, 8 of both
+    // operands
+    constexpr int kSteps = QUANT ? 8 : MB == 1 ? 4 : 2;
+    constexpr int UC = USTEPS * NR >= kSteps ? 1 : kSteps / (USTEPS * NR);
+    using S = Stream<NR, MB, USTEPS, UC, QUANT>;
+    S st;
     extern __shared__ __align__(16) uint8_t smem[];
     float* const red = reinterpret_cast<float*>(smem);  // [wave][tile][lane][4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -161,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
 
     const int64_t KB = g.K / 2, KS = g.K / 32;
     const int nblk = (int)KS;
-    const int units = FAST ? (int)(g.K / 256) : (int)((g.K + 127) / 128);
+    const int units = (int)((g.K + 128 * USTEPS - 1) / (128 * USTEPS));
 
     // ---- tile
     const int nt = g.ntiles;
@@ -227,7 +260,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
             f32x4 part[NR][1];
 #pragma unroll
             for (int i = 0; i < NR; ++i) part[i][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            run_units<NR, 1, FAST, UC>(part, w, a, u0, u1, lg, nblk);
+            st.fetch(w, a, u0, u1, 0, lg, nblk);
+            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
+            st.run(part, w, a, u0, u1, lg, nblk);
 #pragma unroll
             for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -244,7 +279,10 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
         if constexpr (QUANT) {
             // this wave's slice of every row, quantized into its own LDS; the
             // operand reads below see it through pointers that start at unit 0
-            constexpr int kBpu = FAST ? 8 : 4;  // blocks per unit
+            // (after the first weight loads are on their way)
+            st.fetch(w, a, u0, u1, 0, lg, nblk);
+            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
+            constexpr int kBpu = 4 * USTEPS;  // blocks per unit
             const int b0 = u0 * kBpu, blocks = min(u1 * kBpu, nblk) - b0;
             const int rows = MODE == Mode::kPlain ? (int)g.M : 1;
             const int cap = g.slice;  // blocks a wave's row may hold, a multiple of 8
@@ -265,8 +303,10 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
                 if constexpr (MODE == Mode::kGroupUp) r = g.perm[r] / g.top_k;
                 a[m] = {g.a_codes + r * KB, g.a_scales + r * KS};
             }
+            st.fetch(w, a, u0, u1, 0, lg, nblk);
+            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
         }
-        run_units<NR, MB, FAST, UC>(acc, w, a, u0, u1, lg, nblk);
+        st.run(acc, w, a, u0, u1, lg, nblk);
         if constexpr (QUANT) __syncthreads();  // the sums below reuse the slices' LDS
     }
 
@@ -329,39 +369,46 @@ __global__ __launch_bounds__(kThreads) void k_mx_stream(MxStreamArgs g) {
     }
 }
 
-template <int NR, int MB, bool FAST, Mode MODE, bool QUANT>
+// The largest share of one row that a wave quantizes, in blocks, rounded up to
+// 16.
+int slice_of(int64_t K, int usteps, int waves) {
+    const int64_t units = (K + 128 * usteps - 1) / (128 * usteps);
+    return (int)(((units + waves - 1) / waves * 4 * usteps + 15) / 16 * 16);
+}
+
+template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT>
 hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
+    constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
     constexpr bool kUp = MODE == Mode::kSlotUp || MODE == Mode::kGroupUp;
     g.ntiles = (int32_t)(kUp ? (g.N / 2 + 31) / 32 : (g.N + 16 * NR - 1) / (16 * NR));
     const int64_t wgs = mtiles * g.ntiles;
     if (wgs < 1 || wgs >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidValue;
     size_t lds = (size_t)kWaves * NR * MB * 1024;
     if (QUANT) {
-        g.slice = mx_stream_slice(g.K);
+        g.slice = slice_of(g.K, USTEPS, kWaves);
         lds = std::max(lds, (size_t)kWaves * (MODE == Mode::kPlain ? (size_t)g.M : 1) * g.slice * 17);
     }
     if (lds > 64 * 1024) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_mx_stream<NR, MB, FAST, MODE, QUANT>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
+    hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
     return hipGetLastError();
 }
 
 template <int NR, int MB, Mode MODE, bool QUANT>
 hipError_t launch_k(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
-    return g.K % 256 == 0 ? launch_one<NR, MB, true, MODE, QUANT>(g, mtiles, stream)
-                          : launch_one<NR, MB, false, MODE, QUANT>(g, mtiles, stream);
+    // units of four steps where one tile's waves then share them evenly
+    if constexpr (NR == 1 && QUANT)
+        if (g.K % (512 * 8) == 0) return launch_one<NR, MB, 4, MODE, QUANT>(g, mtiles, stream);
+    if (g.K % 256 == 0) return launch_one<NR, MB, 2, MODE, QUANT>(g, mtiles, stream);
+    return launch_one<NR, MB, 1, MODE, QUANT>(g, mtiles, stream);
 }
 
 }  // namespace
 
-int mx_stream_slice(int64_t K) {
-    // the largest share of a wave, in blocks, rounded up to whole units of 8
-    const int64_t units = K % 256 == 0 ? K / 256 : (K + 127) / 128, bpu = K % 256 == 0 ? 8 : 4;
-    const int64_t b = (units + kWaves - 1) / kWaves * bpu;
-    return (int)((b + 7) / 8 * 8);
-}
+// (the largest of the forms: four waves, units of up to four steps)
 bool mx_stream_quantizes(int64_t M, int64_t K) {
-    return M <= 4 && K <= ((int64_t)1 << 20) && (int64_t)kWaves * M * mx_stream_slice(K) * 17 <= 64 * 1024;
+    return M <= 4 && K <= ((int64_t)1 << 20) && (M * (K / 32 + 16 * 8) * 17) <= 64 * 1024;
 }
+bool mx_slots_fit(int64_t H) { return mx_stream_quantizes(1, H); }
 
 hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream) {
     // 16-row weight tiles a workgroup: one while that gives at most 1024
@@ -380,8 +427,7 @@ hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream) {
         return nr == 1 ? launch_k<1, 2, Mode::kPlain, false>(g, 1, stream)
                        : launch_k<2, 2, Mode::kPlain, false>(g, 1, stream);
     if (g.M <= 64)
-        return nr == 1 ? launch_k<1, 4, Mode::kPlain, false>(g, 1, stream)
-                       : launch_k<2, 4, Mode::kPlain, false>(g, 1, stream);
+        return launch_k<1, 4, Mode::kPlain, false>(g, 1, stream);
     return hipErrorInvalidValue;
 }
 
