@@ -68,7 +68,7 @@ struct MxStreamArgs {
     uint16_t* y = nullptr;              // bf16 outputs
     uint8_t* h_codes = nullptr;         // gate/up forms: MXFP4 h [S, N/4], [S, N/64]
     uint8_t* h_scales = nullptr;
-    int32_t ntiles = 0, slice = 0;      // set by the launcher
+    int32_t ntiles = 0, slice = 0, rt = 16;  // set by the launcher
 };
 constexpr int kMxStreamMost = 64;       // activation rows of the plain form
 // Whether the plain form takes bf16 activations of this size, and the slot

@@ -58,15 +58,18 @@ struct Unit {
     Step st[USTEPS];
 };
 
-template <int USTEPS, bool NT>
+// (Plain loads, not non-temporal ones: an instruction reads half a cache line
+// of each row and the next one the other half, which a line that is not kept
+// fetches again: 28.1 against 18.9 us for one token's gate/up product of 8
+// experts, 6144 x 2048.)
+template <int USTEPS>
 __device__ __forceinline__ Unit<USTEPS> load_unit(const RowPtr& r, int unit, int g, int nblk) {
     Unit<USTEPS> u;
     if constexpr (USTEPS > 1) {
         const uint8_t* c = r.codes + (size_t)unit * (64 * USTEPS) + 16 * g;
 #pragma unroll
         for (int i = 0; i < USTEPS; ++i)
-            u.st[i].c = NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c + 64 * i))
-                           : *reinterpret_cast<const u32x4*>(c + 64 * i);
+            u.st[i].c = *reinterpret_cast<const u32x4*>(c + 64 * i);
         uint32_t s[4];
         if constexpr (USTEPS == 4) {
             const uint4 v = *reinterpret_cast<const uint4*>(r.scales + (size_t)unit * 16);
@@ -91,32 +94,38 @@ __device__ __forceinline__ Unit<USTEPS> load_unit(const RowPtr& r, int unit, int
     return u;
 }
 
-// Quantizes `blocks` blocks of one bf16 row (from block b0) into this wave's
-// LDS: codes 16 bytes a block, then scale bytes.
-__device__ __forceinline__ void quantize_slice(const uint16_t* x, int b0, int blocks, uint8_t* lc, uint8_t* ls) {
-    const int lane = threadIdx.x & 63;
-    for (int b = lane; b < blocks; b += 64) {
-        const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)(b0 + b) * 32);
-        uint4 v[4];
-        uint32_t m = 0;
+// A wave quantizes its K slice of `rows` bf16 rows (blocks [b0, b0 + blocks) of
+// each) into its own LDS: codes, `cap` 16-byte blocks a row, then scale bytes.
+// Item i is block i % blocks of row i / blocks.  load() is apart from store()
+// so that the first items can be asked for before the weights, whose loads
+// would otherwise have to return first.
+struct SliceItem {
+    uint4 v[4];
+    __device__ __forceinline__ void load(const uint16_t* x, int64_t K, int b0, int blocks, int i) {
+        const int m = i / blocks, b = i - m * blocks;
+        const uint4* p = reinterpret_cast<const uint4*>(x + m * K + (int64_t)(b0 + b) * 32);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = p[i];
+        for (int q = 0; q < 4; ++q) v[q] = p[q];
+    }
+    __device__ __forceinline__ void store(uint8_t* lc, uint8_t* ls, int cap, int blocks, int i) const {
+        const int m = i / blocks, b = i - m * blocks;
+        uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            m = max_bf16x2(m, v[i].x);
-            m = max_bf16x2(m, v[i].y);
-            m = max_bf16x2(m, v[i].z);
-            m = max_bf16x2(m, v[i].w);
+        for (int q = 0; q < 4; ++q) {
+            mx = max_bf16x2(mx, v[q].x);
+            mx = max_bf16x2(mx, v[q].y);
+            mx = max_bf16x2(mx, v[q].z);
+            mx = max_bf16x2(mx, v[q].w);
         }
-        const uint32_t s = mx_scale_byte(m);
+        const uint32_t s = mx_scale_byte(mx);
         const float d = mx_divisor(s);
         u32x4 o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = mx_encode8(v[i].x, v[i].y, v[i].z, v[i].w, d);
-        *reinterpret_cast<u32x4*>(lc + 16 * b) = o;
-        ls[b] = (uint8_t)s;
+        for (int q = 0; q < 4; ++q) o[q] = mx_encode8(v[q].x, v[q].y, v[q].z, v[q].w, d);
+        *reinterpret_cast<u32x4*>(lc + ((size_t)m * cap + b) * 16) = o;
+        ls[(size_t)m * cap + b] = (uint8_t)s;
     }
-}
+};
 
 // The weights (and packed activations) of UC units in flight.
 template <int NR, int MB, int USTEPS, int UC, bool A_LDS>
@@ -130,10 +139,10 @@ struct Stream {
         for (int c = 0; c < UC; ++c)
             if (u + c < u1) {
 #pragma unroll
-                for (int i = 0; i < NR; ++i) w[buf][c][i] = load_unit<USTEPS, true>(wp[i], u + c, g, nblk);
+                for (int i = 0; i < NR; ++i) w[buf][c][i] = load_unit<USTEPS>(wp[i], u + c, g, nblk);
                 if constexpr (!A_LDS)
 #pragma unroll
-                    for (int m = 0; m < MB; ++m) a[buf][c][m] = load_unit<USTEPS, false>(ap[m], u + c, g, nblk);
+                    for (int m = 0; m < MB; ++m) a[buf][c][m] = load_unit<USTEPS>(ap[m], u + c, g, nblk);
             }
     }
     __device__ __forceinline__ void use(f32x4 (&acc)[NR][MB], const RowPtr (&ap)[MB], int u, int u1, int buf, int g,
@@ -145,7 +154,7 @@ struct Stream {
             Unit<USTEPS> av[MB];
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
-                if constexpr (A_LDS) av[m] = load_unit<USTEPS, false>(ap[m], u + c, g, nblk);
+                if constexpr (A_LDS) av[m] = load_unit<USTEPS>(ap[m], u + c, g, nblk);
                 else av[m] = a[buf][c][m];
             }
 #pragma unroll
@@ -223,12 +232,14 @@ void k_mx_stream(MxStreamArgs g) {
         row_beg = (int64_t)g.row_off[lo] + (mt - g.tile_off[lo]) * (16 * MB);
         row_end = min((int64_t)g.row_off[lo + 1], row_beg + 16 * MB);
     }
-    const int64_t n0 = (int64_t)tn * (kUp ? 32 : 16 * NR);
+    const int64_t n0 = (int64_t)tn * (kUp ? 32 : g.rt * NR);
     const int64_t half = g.N / 2;  // kUp: I
-    // weight rows of tile i; rows past N repeat row n0's tile (never stored)
+    // weight rows of tile i, of which the first rt are the tile's (see
+    // rows_per_tile); others, and rows past N, repeat one and are never stored
+    const int rt = kUp ? 16 : g.rt;
     auto w_row = [&](int i) -> int64_t {
         if constexpr (kUp) return (i < 2 ? 0 : half) + n0 + 16 * (i & 1) + l16;
-        const int64_t n = n0 + 16 * i + l16;
+        const int64_t n = n0 + rt * i + min(l16, rt - 1);
         return n < g.N ? n : g.N - 1;
     };
 
@@ -279,18 +290,22 @@ void k_mx_stream(MxStreamArgs g) {
         if constexpr (QUANT) {
             // this wave's slice of every row, quantized into its own LDS; the
             // operand reads below see it through pointers that start at unit 0
-            // (after the first weight loads are on their way)
-            st.fetch(w, a, u0, u1, 0, lg, nblk);
-            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
             constexpr int kBpu = 4 * USTEPS;  // blocks per unit
-            const int b0 = u0 * kBpu, blocks = min(u1 * kBpu, nblk) - b0;
+            const int b0 = u0 * kBpu, blocks = max(min(u1 * kBpu, nblk) - b0, 0);
             const int rows = MODE == Mode::kPlain ? (int)g.M : 1;
-            const int cap = g.slice;  // blocks a wave's row may hold, a multiple of 8
+            const uint16_t* const x = g.x + (MODE == Mode::kPlain ? 0 : row_beg / g.top_k) * g.K;
+            const int cap = g.slice;  // blocks a wave's row may hold, a multiple of 16
             uint8_t* const lc = smem + (size_t)wave * rows * cap * 17;
             uint8_t* const ls = lc + (size_t)rows * cap * 16;
-            for (int m = 0; m < rows; ++m) {
-                const int64_t src = MODE == Mode::kPlain ? m : row_beg / g.top_k;
-                quantize_slice(g.x + src * g.K, b0, blocks, lc + (size_t)m * cap * 16, ls + (size_t)m * cap);
+            const int items = rows * blocks;
+            SliceItem first;
+            if (lane < items) first.load(x, g.K, b0, blocks, lane);
+            st.fetch(w, a, u0, u1, 0, lg, nblk);
+            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
+            if (lane < items) first.store(lc, ls, cap, blocks, lane);
+            for (int i = lane + 64; i < items; i += 64) {
+                first.load(x, g.K, b0, blocks, i);
+                first.store(lc, ls, cap, blocks, i);
             }
             const int mr = l16 < rows ? l16 : 0;
             a[0] = {lc + ((size_t)mr * cap - b0) * 16, ls + (size_t)mr * cap - b0};
@@ -350,8 +365,8 @@ void k_mx_stream(MxStreamArgs g) {
         for (int p = threadIdx.x; p < NR * MB * 64; p += kThreads) {
             const int t = p >> 6, ln = p & 63;
             const int64_t row = row_beg + 16 * (t % MB) + (ln & 15);
-            const int64_t col = n0 + 16 * (t / MB) + 4 * (ln >> 4);
-            if (row >= row_end || col >= g.N) continue;
+            const int64_t col = n0 + rt * (t / MB) + 4 * (ln >> 4);
+            if (row >= row_end || col >= g.N || 4 * (ln >> 4) >= rt) continue;
             const f32x4 v = total(t, ln);
             {
                 uint16_t* const dst = g.y + row * g.N + col;
@@ -376,11 +391,25 @@ int slice_of(int64_t K, int usteps, int waves) {
     return (int)(((units + waves - 1) / waves * 4 * usteps + 15) / 16 * 16);
 }
 
+// Weight rows of a tile: 16, or 12 or 8 where that spreads the tiles more
+// evenly over the 256 CUs (6144 rows: 384 tiles of 16 leave half the CUs with
+// two and half with one; 512 of 12 give each two: one token through 6144 x
+// 16384 12.9 -> 11.5 us, through the down projection of 8 experts 6144 x 2048
+// 14.5 -> 12.6 us).
+int rows_per_tile(int64_t N, int nr) {
+    auto most = [&](int64_t rt) { return ((N + rt * nr - 1) / (rt * nr) + 255) / 256 * rt; };  // rows of the fullest CU
+    int rt = 16;
+    for (int r = 12; r >= 8; r -= 4)
+        if (most(r) < most(rt)) rt = r;
+    return rt;
+}
+
 template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT>
 hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
     constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
     constexpr bool kUp = MODE == Mode::kSlotUp || MODE == Mode::kGroupUp;
-    g.ntiles = (int32_t)(kUp ? (g.N / 2 + 31) / 32 : (g.N + 16 * NR - 1) / (16 * NR));
+    g.rt = kUp || MODE == Mode::kGroupDown ? 16 : rows_per_tile(g.N, NR);
+    g.ntiles = (int32_t)(kUp ? (g.N / 2 + 31) / 32 : (g.N + g.rt * NR - 1) / (g.rt * NR));
     const int64_t wgs = mtiles * g.ntiles;
     if (wgs < 1 || wgs >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidValue;
     size_t lds = (size_t)kWaves * NR * MB * 1024;
@@ -404,9 +433,11 @@ hipError_t launch_k(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
 
 }  // namespace
 
-// (the largest of the forms: four waves, units of up to four steps)
+// Every workgroup quantizes the rows for itself: 2 us for one row of 16384,
+// 7.5 us for four, against about 4 us for a launch of its own.  (LDS: the
+// largest of the forms, four waves, units of up to four steps.)
 bool mx_stream_quantizes(int64_t M, int64_t K) {
-    return M <= 4 && K <= ((int64_t)1 << 20) && (M * (K / 32 + 16 * 8) * 17) <= 64 * 1024;
+    return M <= 2 && K <= ((int64_t)1 << 20) && (M * (K / 32 + 16 * 8) * 17) <= 64 * 1024;
 }
 bool mx_slots_fit(int64_t H) { return mx_stream_quantizes(1, H); }
 
