@@ -22,7 +22,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "quantize.hip", "transpose.hip", "gemv.hip", "gemm_a16.hip", "gemm_stream.hip", "moe.hip", "lora.hip",
            "mx_api.cpp", "gate.hip", "mx_quant.hip", "mx_gemm.hip",
-           "mx_stream.hip", "mx_combine.hip"]
+           "mx_stream.hip", "mx_route.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

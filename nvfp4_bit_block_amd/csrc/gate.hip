@@ -1,12 +1,20 @@
 // gate.hip -- the expert gate (scores, groups, top-k, weights) and the
 // gradient of its weights.
 //
-// LPT lanes share one token (16 lanes, four tokens a wave, up to 256 experts
-// and top_k 16; the whole wave above that), each holding NPL of its E logits
-// in registers: lane q of the token has experts 4 LPT (i / 4) + 4 q + i % 4,
-// i < NPL, so that four neighbours load as one piece.  top_k rounds of
-// "largest key, lowest expert among equals" pick the experts; every lane of
-// the token sees each winner, and lane j keeps slot j's.
+// LPT lanes share one token, each holding NPL of its E logits in registers: 16
+// lanes, four tokens a wave, for many tokens of up to 256 experts and top_k
+// 16, the whole wave otherwise.  Few tokens are bound by the chain of
+// dependent steps, which a whole wave shortens (one token of 256 experts,
+// sigmoid, bias and groups: 14.3 -> 6.1 us); many by their instructions, of
+// which a quarter wave needs half as many per token.  Lane q of the token has
+// experts 4 LPT (i / 4) + 4 q + i % 4, i < NPL, so that four neighbours load
+// as one piece.  top_k rounds of "largest key, lowest expert among equals"
+// pick the experts; every lane of the token sees each winner, and lane j
+// keeps slot j's.
+//
+// Measured on MI355X: 4096 x 256 fp32, top 8, 6.5 us (a launch takes about 2);
+// the dense gradient of 65536 x 256 bf16, 71 MB read and written, 18.5 us,
+// 3.8 TB/s, bound by its exponentials and the passes through LDS.
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 
@@ -33,55 +41,54 @@ struct GateArgs {
     float scale;
 };
 
-// Reductions over the LPT lanes of a token, the result in all of them.
-template <int LPT>
-__device__ __forceinline__ float tok_max(float v) {
-    v = fmaxf(v, dpp_f32<0xB1>(v));
-    v = fmaxf(v, dpp_f32<0x4E>(v));
-    v = fmaxf(v, dpp_f32<0x141>(v));
-    v = fmaxf(v, dpp_f32<0x140>(v));
-    if constexpr (LPT == 64) {
-        v = fmaxf(v, __shfl_xor(v, 16, kWave));
-        v = fmaxf(v, __shfl_xor(v, 32, kWave));
-    }
+// Reductions over the LPT lanes of a token, the result in all of them: DPP
+// steps within rows of 16 lanes, then the four rows' values through scalars.
+struct OpMax {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+    __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
+};
+struct OpAdd {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+struct OpMin {
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return min(a, b); }
+};
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) { return dpp_u32<CTRL>(v); }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) { return dpp_f32<CTRL>(v); }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp_u32<CTRL>((uint32_t)b) |
+                                          ((uint64_t)dpp_u32<CTRL>((uint32_t)(b >> 32)) << 32));
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ float lane_value(float v, int l) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l));
+}
+__device__ __forceinline__ double lane_value(double v, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)lane_value((uint32_t)b, l) |
+                                          ((uint64_t)lane_value((uint32_t)(b >> 32), l) << 32));
+}
+template <int LPT, typename T, typename Op>
+__device__ __forceinline__ T tok_reduce(T v, Op op) {
+    v = op(v, dpp<0xB1>(v));   // quad_perm [1,0,3,2]
+    v = op(v, dpp<0x4E>(v));   // quad_perm [2,3,0,1]
+    v = op(v, dpp<0x141>(v));  // row_half_mirror
+    v = op(v, dpp<0x140>(v));  // row_mirror
+    if constexpr (LPT == 64)
+        v = op(op(lane_value(v, 0), lane_value(v, 16)), op(lane_value(v, 32), lane_value(v, 48)));
     return v;
 }
+template <int LPT, typename T>
+__device__ __forceinline__ T tok_max(T v) { return tok_reduce<LPT>(v, OpMax()); }
+template <int LPT, typename T>
+__device__ __forceinline__ T tok_sum(T v) { return tok_reduce<LPT>(v, OpAdd()); }
 template <int LPT>
-__device__ __forceinline__ float tok_sum(float v) {
-    v += dpp_f32<0xB1>(v);
-    v += dpp_f32<0x4E>(v);
-    v += dpp_f32<0x141>(v);
-    v += dpp_f32<0x140>(v);
-    if constexpr (LPT == 64) {
-        v += __shfl_xor(v, 16, kWave);
-        v += __shfl_xor(v, 32, kWave);
-    }
-    return v;
-}
-template <int LPT>
-__device__ __forceinline__ uint32_t tok_min(uint32_t v) {
-    v = min(v, dpp_u32<0xB1>(v));
-    v = min(v, dpp_u32<0x4E>(v));
-    v = min(v, dpp_u32<0x141>(v));
-    v = min(v, dpp_u32<0x140>(v));
-    if constexpr (LPT == 64) {
-        v = min(v, (uint32_t)__shfl_xor((int)v, 16, kWave));
-        v = min(v, (uint32_t)__shfl_xor((int)v, 32, kWave));
-    }
-    return v;
-}
-template <int LPT>
-__device__ __forceinline__ double tok_max(double v) {
-#pragma unroll
-    for (int off = LPT / 2; off > 0; off >>= 1) v = fmax(v, __shfl_xor(v, off, kWave));
-    return v;
-}
-template <int LPT>
-__device__ __forceinline__ double tok_sum(double v) {
-#pragma unroll
-    for (int off = LPT / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-    return v;
-}
+__device__ __forceinline__ uint32_t tok_min(uint32_t v) { return tok_reduce<LPT>(v, OpMin()); }
 
 template <int LPT>
 __device__ __forceinline__ int expert_of(int q, int i) {
@@ -211,24 +218,36 @@ __global__ __launch_bounds__(gate_threads(LPT)) void k_gate(GateArgs a) {
     }
 
     if (a.n_group > a.topk_group) {
-        // ranks of the groups, from the keys in LDS: lane g takes group g, g + LPT, ..
+        // ranks of the groups, from the keys in LDS: P lanes per group (a power
+        // of two, as many as the groups leave), lane p takes members p, p + P, ..
         Key* const ks = reinterpret_cast<Key*>(smem) + (size_t)tl * (a.E + a.n_group);
         Key* const rank = ks + a.E;
+        const Key none = -(Key)__builtin_inf();
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = expert_of<LPT>(q, i);
             if (e < a.E) ks[e] = key[i];
         }
         __syncthreads();
-        for (int g = q; g < a.n_group; g += LPT) {
-            Key b1 = -(Key)__builtin_inf(), b2 = b1;
-            for (int i = 0; i < a.members; ++i) {
-                const Key v = ks[g * a.members + i];
-                b2 = v > b1 ? b1 : (v > b2 ? v : b2);
-                b1 = v > b1 ? v : b1;
+        int P = LPT;
+        while (P > 1 && P * a.n_group > LPT) P >>= 1;
+        const int gq = q / P, p = q & (P - 1);
+        for (int g0 = 0; g0 < a.n_group; g0 += LPT / P) {
+            const int g = g0 + gq;
+            Key b1 = none, b2 = none;
+            if (g < a.n_group)
+                for (int i = p; i < a.members; i += P) {
+                    const Key v = ks[g * a.members + i];
+                    b2 = v > b1 ? b1 : (v > b2 ? v : b2);
+                    b1 = v > b1 ? v : b1;
+                }
+            for (int off = 1; off < P; off <<= 1) {
+                const Key o1 = __shfl_xor(b1, off, kWave), o2 = __shfl_xor(b2, off, kWave);
+                b2 = o1 > b1 ? (b1 > o2 ? b1 : o2) : (o1 > b2 ? o1 : b2);
+                b1 = o1 > b1 ? o1 : b1;
             }
-            if (a.group_top == 2 && b2 > -(Key)__builtin_inf()) b1 += b2;
-            rank[g] = b1;
+            if (a.group_top == 2 && b2 > none) b1 += b2;
+            if (p == 0 && g < a.n_group) rank[g] = b1;
         }
         __syncthreads();
         // a group stays if fewer than topk_group groups come before it
@@ -239,14 +258,13 @@ __global__ __launch_bounds__(gate_threads(LPT)) void k_gate(GateArgs a) {
                 const Key o = rank[h];
                 before += o > r || (o == r && h < g);
             }
-            if (before >= a.topk_group)
-                for (int i = 0; i < a.members; ++i) ks[g * a.members + i] = -(Key)__builtin_inf();
+            ks[g] = (Key)(before < a.topk_group ? 1 : 0);  // (the keys are in registers)
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = expert_of<LPT>(q, i);
-            if (e < a.E) key[i] = ks[e];
+            if (e < a.E && ks[(uint32_t)e / (uint32_t)a.members] == (Key)0) key[i] = none;
         }
     }
 
@@ -315,7 +333,9 @@ __global__ __launch_bounds__(gate_threads(LPT)) void k_gate_backward(GateArgs a)
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            l[i] = expf(l[i] - m);
+            // (a bf16 gradient keeps 8 bits: the hardware's exponential, a few
+            // parts in 2^22 at the arguments that matter, is exact enough)
+            l[i] = BF16 ? __builtin_amdgcn_exp2f(1.44269504f * (l[i] - m)) : expf(l[i] - m);
             s += l[i];
         }
         z = fmaxf(tok_sum<LPT>(s), 1e-30f);
@@ -333,10 +353,13 @@ __global__ __launch_bounds__(gate_threads(LPT)) void k_gate_backward(GateArgs a)
         const float og = __shfl(g, src, kWave);
         gs += oid == id ? og : 0.0f;
     }
+    const float share = kDense ? -dot / z : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
+    for (int i = 0; i < NPL; i += 4) {
         const int e = expert_of<LPT>(q, i);
-        if (e < a.E) row[e] = kDense ? -dot * (l[kDense ? i : 0] / z) : 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if constexpr (kDense) v = make_float4(share * l[i], share * l[i + 1], share * l[i + 2], share * l[i + 3]);
+        if (e < a.E) *reinterpret_cast<float4*>(row + e) = v;  // (rows are padded to fours)
     }
     __syncthreads();
     if (id >= 0) row[id] += gs;  // equal ids store equal sums
@@ -403,11 +426,14 @@ hipError_t gate_dispatch(const nvfp4_gate_config& c, GateArgs a, bool backward, 
     a.E = (int32_t)c.E;
     a.top_k = (int32_t)c.top_k;
     a.scale = c.scale;
-    if (c.E <= 256 && c.top_k <= 16) {
+    // (measured with E = 256, top_k 8 on MI355X: see the file's head; the
+    // gradient's row passes want whole waves of tokens at any T)
+    if (c.E <= 256 && c.top_k <= 16 && (backward || c.T > 2048)) {
         if (c.E <= 64) return gate_types<16, 4>(c, a, backward, s);
         if (c.E <= 128) return gate_types<16, 8>(c, a, backward, s);
         return gate_types<16, 16>(c, a, backward, s);
     }
+    if (c.E <= 256) return gate_types<64, 4>(c, a, backward, s);
     if (c.E <= 512) return gate_types<64, 8>(c, a, backward, s);
     if (c.E <= 1024) return gate_types<64, 16>(c, a, backward, s);
     return gate_types<64, 64>(c, a, backward, s);

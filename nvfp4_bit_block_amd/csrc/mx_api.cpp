@@ -124,8 +124,10 @@ MxMoeLayout layout_mx_moe(const nvfp4_mx_moe_problem& p) {
     l.tile_off = off; off += align_up((size_t)(p.E + 1) * 4);
     l.perm = off; off += align_up((size_t)S * 4);
     l.inv = off; off += align_up((size_t)S * 4);
-    l.pos_group = off; off += align_up((size_t)S * 4);
-    l.route = off; off += align_up(moe_route_scratch_bytes(S, (int32_t)p.E));
+    if (S > kMxPrepareSlots) {
+        l.pos_group = off; off += align_up((size_t)S * 4);
+        l.route = off; off += align_up(moe_route_scratch_bytes(S, (int32_t)p.E));
+    }
     l.xc = off; off += packed_codes_bytes(p.T, p.H);
     l.xs = off; off += packed_scales_bytes(p.T, p.H);
     l.hc = off; off += packed_codes_bytes(S, p.I);
@@ -346,12 +348,20 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
     uint8_t* hc = at<uint8_t>(workspace, l.hc);
     uint8_t* hs = at<uint8_t>(workspace, l.hs);
     uint16_t* Y = at<uint16_t>(workspace, l.y);
-    int32_t st = api_hip(launch_moe_route(t->topk_ids, S, E, bm, row_off, tile_off, perm, inv,
-                                          at<int32_t>(workspace, l.pos_group), at<int32_t>(workspace, l.route), s),
-                         "mx_moe route");
-    if (st) return st;
-    st = api_hip(launch_mx_quantize(t->x, p->T, p->H, xc, xs, s), "mx_moe quantize");
-    if (st) return st;
+    int32_t st;
+    if (S <= kMxPrepareSlots) {
+        const MxPrepareArgs a = {t->topk_ids, (int32_t)S, E, bm, row_off, tile_off, perm, inv, t->x, p->T * (p->H / 8),
+                                 xc, xs};
+        st = api_hip(launch_mx_prepare(a, s), "mx_moe prepare");
+        if (st) return st;
+    } else {
+        st = api_hip(launch_moe_route(t->topk_ids, S, E, bm, row_off, tile_off, perm, inv,
+                                      at<int32_t>(workspace, l.pos_group), at<int32_t>(workspace, l.route), s),
+                     "mx_moe route");
+        if (st) return st;
+        st = api_hip(launch_mx_quantize(t->x, p->T, p->H, xc, xs, s), "mx_moe quantize");
+        if (st) return st;
+    }
     const int grid_m = (int)((S + bm - 1) / bm + std::min<int64_t>(E, S));
     if (plan != MoePlan::kTiles) {
         up.a_codes = xc;

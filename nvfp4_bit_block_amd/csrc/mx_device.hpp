@@ -62,6 +62,16 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t m, uint32_t w) {
     return max(max(m, w & 0x7FFFu), (w >> 16) & 0x7FFFu);
 }
 
+// Eight elements per lane, a block per quad of lanes (all four active): this
+// lane's codes and the block's scale byte.
+__device__ __forceinline__ void mx_encode_quad(const uint4& v, uint32_t& code, uint32_t& s) {
+    uint32_t m = max_bf16x2(max_bf16x2(max_bf16x2(max_bf16x2(0, v.x), v.y), v.z), v.w);
+    m = max(m, dpp_u32<0xB1>(m));  // quad_perm [1,0,3,2]
+    m = max(m, dpp_u32<0x4E>(m));  // quad_perm [2,3,0,1]
+    s = mx_scale_byte(m);
+    code = mx_encode8(v.x, v.y, v.z, v.w, mx_divisor(s));
+}
+
 // The group whose row tiles [tile_off[e], tile_off[e + 1]) hold tile `mt`
 // (which some group's do): a wave compares 64 bounds at a time, so 4096
 // groups take two dependent loads.

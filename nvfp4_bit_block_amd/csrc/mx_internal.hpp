@@ -82,6 +82,27 @@ hipError_t launch_mx_slot_down(const MxStreamArgs& g, int64_t tokens, hipStream_
 hipError_t launch_mx_group_up(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
 hipError_t launch_mx_group_down(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
 
+// The sorted routed layer's first launch (mx_route.hip): row_off and tile_off
+// [E + 1] (tiles of bm rows), the slot of each expert row perm [slots] and the
+// row of each slot inv [slots] (-1 for an id outside [0, E)); and the MXFP4 of
+// the tokens x, n8 pieces of 8 elements.  E <= 4096.  One workgroup sorts, so
+// at most kMxPrepareSlots slots (its scattered stores take 32 us at 32768,
+// where three launches and the quantizer take 25).
+struct MxPrepareArgs {
+    const int32_t* ids;
+    int32_t slots, E, bm;
+    int32_t* row_off;
+    int32_t* tile_off;
+    int32_t* perm;
+    int32_t* inv;
+    const uint16_t* x;
+    int64_t n8;
+    uint8_t* codes;
+    uint8_t* scales;
+};
+constexpr int64_t kMxPrepareSlots = 1 << 13;
+hipError_t launch_mx_prepare(const MxPrepareArgs& a, hipStream_t stream);
+
 // out[t] = bf16(sum_j w[t, j] * Y[inv[t * top_k + j]]) over expert-sorted bf16
 // rows Y [S, H], slots in order, inv < 0 skipped; H % 32 == 0.
 hipError_t launch_mx_combine(const uint16_t* Y, const int32_t* inv, const float* w, int64_t T, int32_t top_k, int64_t H,

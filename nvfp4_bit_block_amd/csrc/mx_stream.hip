@@ -395,7 +395,8 @@ int slice_of(int64_t K, int usteps, int waves) {
 // evenly over the 256 CUs (6144 rows: 384 tiles of 16 leave half the CUs with
 // two and half with one; 512 of 12 give each two: one token through 6144 x
 // 16384 12.9 -> 11.5 us, through the down projection of 8 experts 6144 x 2048
-// 14.5 -> 12.6 us).
+// 14.5 -> 12.6 us).  With more than 16 activation rows a workgroup's reads of
+// them count, and fewer, whole tiles win (37 x 4099 x 2080: 6.0 against 7.1).
 int rows_per_tile(int64_t N, int nr) {
     auto most = [&](int64_t rt) { return ((N + rt * nr - 1) / (rt * nr) + 255) / 256 * rt; };  // rows of the fullest CU
     int rt = 16;
@@ -408,7 +409,7 @@ template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT>
 hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
     constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
     constexpr bool kUp = MODE == Mode::kSlotUp || MODE == Mode::kGroupUp;
-    g.rt = kUp || MODE == Mode::kGroupDown ? 16 : rows_per_tile(g.N, NR);
+    g.rt = kUp || MODE == Mode::kGroupDown || MB > 1 ? 16 : rows_per_tile(g.N, NR);
     g.ntiles = (int32_t)(kUp ? (g.N / 2 + 31) / 32 : (g.N + g.rt * NR - 1) / (g.rt * NR));
     const int64_t wgs = mtiles * g.ntiles;
     if (wgs < 1 || wgs >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidValue;
