@@ -54,15 +54,18 @@ int32_t check_product(int64_t M, int64_t N, int64_t K) {
     return NVFP4_OK;
 }
 
-// Up to 64 activation rows run on the weight-streaming kernel, more on the
-// LDS tiles.
-bool streams(int64_t M) { return M <= kMxStreamMost; }
 // A bf16 activation that the streaming kernel quantizes itself.
-bool one_launch(int64_t M, int64_t K) { return streams(M) && mx_stream_quantizes(M, K); }
+bool one_launch(int64_t M, int64_t N, int64_t K) { return mx_stream_takes(M, N, K) && mx_stream_quantizes(M, K); }
+
+size_t partial_bytes(int64_t M, int64_t N, int64_t K) {
+    int steps;
+    const int splits = mx_stream_takes(M, N, K) ? 1 : mx_gemm_splits(M, N, K, &steps);
+    return splits > 1 ? align_up((size_t)splits * (size_t)(M * N) * 4) : 0;
+}
 
 hipError_t run_product(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int64_t N, int64_t K,
-                       const uint8_t* w_codes, const uint8_t* w_scales, uint16_t* y, hipStream_t s) {
-    if (streams(M)) {
+                       const uint8_t* w_codes, const uint8_t* w_scales, uint16_t* y, float* partial, hipStream_t s) {
+    if (mx_stream_takes(M, N, K)) {
         MxStreamArgs g;
         g.a_codes = a_codes;
         g.a_scales = a_scales;
@@ -84,6 +87,7 @@ hipError_t run_product(const uint8_t* a_codes, const uint8_t* a_scales, int64_t 
     g.K = K;
     g.out = y;
     g.ldo = N;
+    if (partial_bytes(M, N, K) > 0) return launch_mx_gemm_split(g, partial, s);
     return launch_mx_gemm(g, MxEpi::kStoreBf16, 0, s);
 }
 
@@ -227,8 +231,8 @@ int32_t nvfp4_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t
 }
 
 size_t nvfp4_mx_gemm_packed_workspace_size(int64_t M, int64_t N, int64_t K) {
-    (void)M; (void)N; (void)K;
-    return 0;
+    if (M <= 0 || N <= 0 || check_product(M, N, K) != NVFP4_OK) return 0;
+    return partial_bytes(M, N, K);
 }
 
 int32_t nvfp4_mx_gemm_packed(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int64_t N, int64_t K,
@@ -245,13 +249,13 @@ int32_t nvfp4_mx_gemm_packed(const uint8_t* a_codes, const uint8_t* a_scales, in
     const size_t need = nvfp4_mx_gemm_packed_workspace_size(M, N, K);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return api_fail(NVFP4_ERR_WORKSPACE, "mx_gemm_packed: workspace smaller than nvfp4_mx_gemm_packed_workspace_size");
-    return api_hip(run_product(a_codes, a_scales, M, N, K, w_codes, w_scales, y, as_stream(stream)), "mx_gemm_packed");
+    return api_hip(run_product(a_codes, a_scales, M, N, K, w_codes, w_scales, y, at<float>(workspace, 0), as_stream(stream)), "mx_gemm_packed");
 }
 
 size_t nvfp4_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || check_product(M, N, K) != NVFP4_OK) return 0;
-    if (one_launch(M, K)) return 0;
-    return packed_codes_bytes(M, K) + packed_scales_bytes(M, K);
+    if (M <= 0 || N <= 0 || check_product(M, N, K) != NVFP4_OK) return 0;
+    if (one_launch(M, N, K)) return 0;
+    return packed_codes_bytes(M, K) + packed_scales_bytes(M, K) + partial_bytes(M, N, K);
 }
 
 int32_t nvfp4_mx_gemm(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
@@ -268,7 +272,7 @@ int32_t nvfp4_mx_gemm(const uint16_t* x, int64_t M, int64_t N, int64_t K, const 
     if (need > 0 && (!workspace || workspace_bytes < need))
         return api_fail(NVFP4_ERR_WORKSPACE, "mx_gemm: workspace smaller than nvfp4_mx_gemm_workspace_size");
     hipStream_t s = as_stream(stream);
-    if (one_launch(M, K)) {
+    if (one_launch(M, N, K)) {
         MxStreamArgs g;
         g.x = x;
         g.b_codes = w_codes;
@@ -282,7 +286,8 @@ int32_t nvfp4_mx_gemm(const uint16_t* x, int64_t M, int64_t N, int64_t K, const 
     uint8_t* const xc = at<uint8_t>(workspace, 0);
     uint8_t* const xs = at<uint8_t>(workspace, packed_codes_bytes(M, K));
     if (int32_t st = api_hip(launch_mx_quantize(x, M, K, xc, xs, s), "mx_gemm quantize")) return st;
-    return api_hip(run_product(xc, xs, M, N, K, w_codes, w_scales, y, s), "mx_gemm");
+    float* const partial = at<float>(workspace, packed_codes_bytes(M, K) + packed_scales_bytes(M, K));
+    return api_hip(run_product(xc, xs, M, N, K, w_codes, w_scales, y, partial, s), "mx_gemm");
 }
 
 size_t nvfp4_mx_moe_workspace_size(const nvfp4_mx_moe_problem* p) {

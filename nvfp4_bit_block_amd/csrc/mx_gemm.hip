@@ -69,6 +69,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     constexpr int LDS = SC_OFF + 2 * SC_HALF;
     static_assert(LDS <= 160 * 1024, "LDS");
     constexpr bool kGateUp = EP == MxEpi::kGateUp;
+    constexpr bool kSplit = EP == MxEpi::kPartialF32;
     static_assert(!kGateUp || TN % 2 == 0, "gate/up pairs column blocks");
     __shared__ __align__(1024) uint8_t smem[LDS];
 
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     // ---- tile.  Workgroups reach the 8 XCDs round-robin by id; renumber so
     // that each XCD has a contiguous run of the real tiles.
     const int gm_tiles = g.groups > 0 ? g.tile_off[g.groups] : (int)((g.M + BM - 1) / BM);
-    const int64_t total = (int64_t)gm_tiles * g.ntiles;
+    const int64_t tiles = (int64_t)gm_tiles * g.ntiles, total = tiles * (kSplit ? g.ksplit : 1);
     int64_t id = blockIdx.x;
     if ((gridDim.x & 7) == 0) {
         const int64_t per = (total + 7) >> 3, j = id >> 3;
@@ -88,6 +89,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
         id = (id & 7) * per + j;
     }
     if (id >= total) return;
+    int kz = 0;
+    if constexpr (kSplit) {
+        kz = (int)(id / tiles);
+        id -= kz * tiles;
+    }
     int grp = 0, tn;
     int64_t row_beg, row_end;
     if (g.groups > 0) {
@@ -110,8 +116,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     }
 
     const uint32_t KB = (uint32_t)(g.K / 2), KS = (uint32_t)(g.K / 32);
-    const int nsteps = (int)((KS + 7) / 8);
-    const int tail = (int)(KS - 8 * (uint32_t)(nsteps - 1));  // blocks of the last step, 1 .. 8
+    // this workgroup's K steps [k0, k0 + nsteps) of ksteps (k0 a multiple of
+    // RSTEP)
+    const int ksteps = (int)((KS + 7) / 8), k0 = kSplit ? kz * g.ksteps : 0;
+    const int nsteps = kSplit ? min(g.ksteps, ksteps - k0) : ksteps;
+    const int tail = (int)(KS - 8 * (uint32_t)(ksteps - 1));  // blocks of the last step, 1 .. 8
 
     // First weight row of the tile, and tile row n's row relative to it (-1
     // past the end).  Gate/up: each wave holds gate blocks, then the matching
@@ -156,8 +165,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     }
     // scales.  ALIGNED: slab sl holds tile rows SCR sl + lane / LPR (the
     // activations', then the weights'), 16 bytes lane % LPR of theirs; in
-    // phase p a wave loads slab p NW + wave.  Otherwise thread t carries tile rows t, t + NT, .. of one step through registers,
-    // from a base rounded down to a word.
+    // phase p a wave loads slab p NW + wave.  Otherwise thread t carries tile
+    // rows t, t + NT, .. of one step through registers, as the aligned words
+    // that hold its bytes (so up to three bytes next to the tensor's are read).
     const uint8_t* const as = g.a_scales + a0 * KS;
     const uint8_t* const bs = g.b_scales + ((int64_t)grp * g.N + n0) * KS;
     const uint32_t da = ALIGNED ? 0u : (uint32_t)(uintptr_t)as & 3u, db = ALIGNED ? 0u : (uint32_t)(uintptr_t)bs & 3u;
@@ -173,10 +183,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
         vs[u] = src < 0 ? kOob : (uint32_t)src * KS + (ALIGNED ? 16u * (lane % LPR) : r < BM ? da : db);
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
-    // Phase ph of the scales of steps RSTEP q .. RSTEP (q + 1) - 1 (a
-    // phase too many repeats the last).  The bytes may run past
-    // the row, whose neighbour's bytes no step uses, and past the tensor, where the
-    // range check, made word by word, gives zeros.
+    // Phase ph of the scales of steps RSTEP q .. RSTEP (q + 1) - 1 (a phase too
+    // many repeats the last).  The bytes may run past the row, whose
+    // neighbour's bytes no step uses, and past the tensor, where the range
+    // check, made word by word, gives zeros.
     auto issue_scales = [&](int ph, int q) {
         if constexpr (ALIGNED) {
             ph = min(ph, PHASES - 1);
@@ -190,19 +200,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
             r.y = __builtin_amdgcn_readfirstlane(r.y);
             r.z = __builtin_amdgcn_readfirstlane(r.z);
             r.w = kRsrcWord3;
-            lds_load16(r, v + (uint32_t)(SCB * q), 0u, lds0 + (uint32_t)(SC_OFF + (q & 1) * SC_HALF + 1024 * sl));
+            lds_load16(r, v + (uint32_t)(SCB * q + 8 * k0), 0u, lds0 + (uint32_t)(SC_OFF + (q & 1) * SC_HALF + 1024 * sl));
         }
     };
     auto load_scales = [&](int kc) {
         if constexpr (!ALIGNED) {
-            const int nb = kc + 1 < nsteps ? 8 : tail;
+            const int nb = k0 + kc + 1 < ksteps ? 8 : tail;
             const uint32_t m0 = nb >= 4 ? ~0u : (1u << (8 * nb)) - 1u;
             const uint32_t m1 = nb >= 8 ? ~0u : nb <= 4 ? 0u : (1u << (8 * (nb - 4))) - 1u;
 #pragma unroll
             for (int u = 0; u < SC_PER_T; ++u) {
                 // (rows of one wave are all activations or all weights)
                 const u32x4 rr = __builtin_amdgcn_readfirstlane(tid + u * NT) < BM ? rsa : rsb;
-                const uint32_t at = vs[u] + 8u * (uint32_t)kc, sh = 8u * (at & 3u);
+                const uint32_t at = vs[u] + 8u * (uint32_t)(k0 + kc), sh = 8u * (at & 3u);
                 const u32x4 d = __builtin_amdgcn_raw_buffer_load_b128(
                     __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)rr.y << 32) | rr.x), 0, (int)rr.z, (int)rr.w),
                     (int)(at & ~3u), 0, 0);
@@ -227,11 +237,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     // steps past the last load nothing: a resource of no bytes, at offset zero
     // so that the range check holds whichever way it counts the offset.
     auto issue = [&](int p, int kc, uint32_t at) {
-        const bool live = kc < nsteps, last = kc + 1 == nsteps;
+        const bool live = kc < nsteps, last = k0 + kc + 1 == ksteps;
         u32x4 r = p < CA ? ra : rb;
         r.z = __builtin_amdgcn_readfirstlane(live ? r.z : 0u);
         const uint32_t cut = last && chunk_of(slab(p)) >= tail ? kOob : 0u;
-        lds_load16(r, vc[p] | cut, live ? (uint32_t)kc * 128u : 0u, lds0 + at + (uint32_t)(slab(p) * 1024));
+        lds_load16(r, vc[p] | cut, live ? (uint32_t)(k0 + kc) * 128u : 0u, lds0 + at + (uint32_t)(slab(p) * 1024));
     };
 
     f32x16 acc[TN][TM];
@@ -244,11 +254,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
 
     // ---- main loop.  The fragments of the next instruction are read among
     // the instructions of this one, into the other half of the fragment
-    // registers.  The step's barrier stands before its last instructions: by then
-    // every fragment of the step is in registers, so the stage is free, and
-    // the next step has landed (only the loads of the steps after it may be
-    // out); those last instructions cover the first reads of the next
-    // step and the issue of the loads into the freed stage.  The scheduling
+    // registers.  The step's barrier stands before its last instructions: by
+    // then every fragment of the step is in registers, so the stage is free,
+    // and the next step has landed (only the loads of the steps after it may
+    // be out); those last instructions cover the first reads of the next step
+    // and the issue of the loads into the freed stage.  The scheduling
     // barriers keep that order, and the body must not branch: the matrix
     // instructions, which the compiler sees without side effects, otherwise
     // sink below the last branch and nothing overlaps (325 us against 239 us
@@ -295,7 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
             const uint32_t at = (uint32_t)(((kc / RSTEP) & 1) * SC_HALF + 8 * (kc % RSTEP));
             // (blocks 4 .. 7 of a last step without them: zero, not the bytes
             // after the row)
-            const uint32_t keep = kc + 1 == nsteps && 4 * hf >= tail ? 0u : ~0u;
+            const uint32_t keep = k0 + kc + 1 == ksteps && 4 * hf >= tail ? 0u : ~0u;
 #pragma unroll
             for (int i = 0; i < TA; ++i)
                 xa[i] = *reinterpret_cast<const uint32_t*>(smem + (at + sa_off) + 32 * SCB * WM * i) & keep;
@@ -402,6 +412,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
                     if (hf == 0) g.out_scales[row * (g.ldo / 32) + hc / 32] = (uint8_t)s;
                 }
             }
+        } else if constexpr (kSplit) {
+            if (row >= row_end) continue;
+            float* const out = reinterpret_cast<float*>(g.out) + ((int64_t)kz * g.M + row) * g.ldo;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int64_t col = n0 + wn * WTN + 32 * j + 8 * p + 4 * hf;
+                    if ((g.ldo & 3) == 0) {
+                        if (col < nlim)
+                            *reinterpret_cast<f32x4*>(out + col) = f32x4{acc[j][i][4 * p], acc[j][i][4 * p + 1],
+                                                                         acc[j][i][4 * p + 2], acc[j][i][4 * p + 3]};
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (col + q < nlim) out[col + q] = acc[j][i][4 * p + q];
+                    }
+                }
         } else {
             // a 32-row slab of the wave's tile meets in LDS and leaves as
             // 16-byte pieces of rows (pitch: 16 rows' 8-byte writes fall on
@@ -448,7 +476,7 @@ hipError_t launch_cfg(const MxGemmArgs& g0, int grid_m, hipStream_t stream) {
     const int64_t ncols = EP == MxEpi::kGateUp ? g.N / 2 : g.N, bn = EP == MxEpi::kGateUp ? BN / 2 : BN;
     g.ntiles = (int32_t)((ncols + bn - 1) / bn);
     const int64_t mt = g.groups > 0 ? grid_m : (g.M + BM - 1) / BM;
-    int64_t wgs = mt * g.ntiles;
+    int64_t wgs = mt * g.ntiles * (EP == MxEpi::kPartialF32 ? g.ksplit : 1);
     if (g.groups > 0) wgs = (wgs + 7) / 8 * 8;  // a multiple of 8 for the XCD renumbering
     if (wgs < 1 || wgs >= ((int64_t)1 << 32) / (64 * WM * WN)) return hipErrorInvalidValue;
     if (ONLY_ALIGNED && g.K % 128 != 0) return hipErrorInvalidValue;
@@ -459,7 +487,50 @@ hipError_t launch_cfg(const MxGemmArgs& g0, int grid_m, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// y[i] = bf16(sum over the K splits, in order); four elements a thread.
+__global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int ksplit, int64_t n,
+                                                 uint16_t* __restrict__ y) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    if ((n & 3) == 0) {
+        f32x4 s = *reinterpret_cast<const f32x4*>(part + i);
+        for (int k = 1; k < ksplit; ++k) s += *reinterpret_cast<const f32x4*>(part + k * n + i);
+        *reinterpret_cast<uint2*>(y + i) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+    } else {
+        for (int64_t e = i; e < n && e < i + 4; ++e) {
+            float s = part[e];
+            for (int k = 1; k < ksplit; ++k) s += part[k * n + e];
+            y[e] = (uint16_t)pack_bf16(s, 0.0f);
+        }
+    }
+}
+
 }  // namespace
+
+// K splits of the 128 x 128 tiles: while the tiles leave CUs without one and
+// every split keeps eight K steps (64 rows x 6144 x 16384 in 10 splits: 22 us;
+// 256 rows x 16384 x 2048, 256 tiles of 8 steps, in two: 25 us against 15
+// unsplit).
+int mx_gemm_splits(int64_t M, int64_t N, int64_t K, int* steps) {
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), ksteps = (K + 255) / 256;
+    int64_t s = std::min<int64_t>({512 / std::max<int64_t>(tiles, 1), ksteps / 8, 16});
+    if (s < 2 || tiles >= 256) return 1;
+    const int64_t per = ((ksteps + s - 1) / s + 3) / 4 * 4;  // a multiple of the scale ring's four steps
+    *steps = (int)per;
+    return (int)((ksteps + per - 1) / per);
+}
+
+hipError_t launch_mx_gemm_split(const MxGemmArgs& g0, float* partial, hipStream_t stream) {
+    MxGemmArgs g = g0;
+    g.ksplit = mx_gemm_splits(g.M, g.N, g.K, &g.ksteps);
+    g.out = partial;
+    hipError_t e = launch_cfg<2, 2, 2, 2, 2, 4, MxEpi::kPartialF32>(g, 0, stream);
+    if (e != hipSuccess) return e;
+    const int64_t n = g.M * g.N;
+    hipLaunchKernelGGL(k_mx_join, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, stream, partial, g.ksplit, n,
+                       reinterpret_cast<uint16_t*>(g0.out));
+    return hipGetLastError();
+}
 
 // Tiles, measured on MI355X with random codes (TFLOP/s; N x K 6144 x 16384 at
 // M = 4096 and 1024, 16384 x 2048 at M = 4096):

@@ -24,6 +24,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 enum class MxEpi : int {
     kStoreBf16 = 0,  // y = bf16(acc)
     kGateUp = 1,     // h = bf16(silu(g) * u), stored as MXFP4
+    kPartialF32 = 2, // partial[split] = acc (K split, joined afterwards)
 };
 
 struct MxGemmArgs {
@@ -41,6 +42,7 @@ struct MxGemmArgs {
     const int32_t* tile_off = nullptr;
     int32_t groups = 0;
     int32_t ntiles = 0;                 // set by the launcher
+    int32_t ksplit = 1, ksteps = 0;     // kPartialF32: K splits and the steps of each
     void* out = nullptr;                // kStoreBf16: bf16 [M, ldo]; kGateUp: codes [M, ldo/2]
     uint8_t* out_scales = nullptr;      // kGateUp: [M, ldo/32]
     int64_t ldo = 0;
@@ -50,6 +52,10 @@ struct MxGemmArgs {
 constexpr int kMxMoeBM = 192;
 // grid_m bounds the row tiles of a grouped launch (ungrouped: ignored).
 hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream);
+// The K splits that launch_mx_gemm_split makes of a plain product (1: none) and
+// the steps of each; it holds that many [M, N] fp32 sums in `partial`.
+int mx_gemm_splits(int64_t M, int64_t N, int64_t K, int* steps);
+hipError_t launch_mx_gemm_split(const MxGemmArgs& g, float* partial, hipStream_t stream);
 
 // Few activation rows (mx_stream.hip).
 struct MxStreamArgs {
@@ -70,9 +76,10 @@ struct MxStreamArgs {
     uint8_t* h_scales = nullptr;
     int32_t ntiles = 0, slice = 0, rt = 16;  // set by the launcher
 };
-constexpr int kMxStreamMost = 64;       // activation rows of the plain form
-// Whether the plain form takes bf16 activations of this size, and the slot
-// forms tokens of this width (they quantize them into LDS).
+// Whether the plain form is the one to run (at most 64 activation rows), and
+// whether it takes bf16 activations of this size, and the slot forms tokens of
+// this width (they quantize them into LDS).
+bool mx_stream_takes(int64_t M, int64_t N, int64_t K);
 bool mx_stream_quantizes(int64_t M, int64_t K);
 bool mx_slots_fit(int64_t H);
 hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream);

@@ -442,11 +442,28 @@ bool mx_stream_quantizes(int64_t M, int64_t K) {
 }
 bool mx_slots_fit(int64_t H) { return mx_stream_quantizes(1, H); }
 
+// 16-row weight tiles of a wave in the plain form: one while that gives at most
+// 512 workgroups or the rows are long, else two or (up to 16 activation rows)
+// four.
+static int plain_tiles(int64_t M, int64_t N, int64_t K) {
+    const int64_t t1 = (N + 15) / 16;
+    const int nr = t1 <= 512 || K >= 8192 ? 1 : t1 <= 1024 ? 2 : 4;
+    return M <= 16 ? nr : M <= 32 ? std::min(nr, 2) : 1;
+}
+
+// Every workgroup reads the activation, so with more rows that becomes the
+// larger stream: at 6144 x 16384 4 rows take 16.7 us, 8 18.6, 16 22 and 64 57,
+// where the LDS tiles take 17 for up to 16 and 21 for 64; 32 rows of 16384 x
+// 2048 take 10 us either way.
+bool mx_stream_takes(int64_t M, int64_t N, int64_t K) {
+    if (M > 64) return false;
+    if (M <= 4) return true;
+    const int64_t nr = plain_tiles(M, N, K), wgs = (N + 16 * nr - 1) / (16 * nr);
+    return wgs <= ((int64_t)20 << 20) / (M * (K / 2));
+}
+
 hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream) {
-    // 16-row weight tiles a workgroup: one while that gives at most 1024
-    // workgroups or the rows are long, else two or four
-    const int64_t t1 = (g.N + 15) / 16;
-    const int nr = t1 <= 512 || g.K >= 8192 ? 1 : t1 <= 1024 ? 2 : 4;
+    const int nr = plain_tiles(g.M, g.N, g.K);
     if (g.x != nullptr)
         return nr == 1 ? launch_k<1, 1, Mode::kPlain, true>(g, 1, stream)
                        : nr == 2 ? launch_k<2, 1, Mode::kPlain, true>(g, 1, stream)

@@ -94,7 +94,8 @@ def _check_product(y, a, w):
 
 SHAPES = [(1, 16, 32), (1, 1, 64), (1, 257, 4096), (2, 40, 96), (5, 4099, 512), (8, 100, 2080), (16, 64, 1024),
           (17, 33, 544), (33, 130, 256), (64, 256, 768), (100, 70, 1312), (128, 128, 512), (129, 257, 288),
-          (300, 515, 2048), (257, 256, 8192), (31, 1, 32)]
+          (300, 515, 2048), (257, 256, 8192), (31, 1, 32),
+          (65, 129, 4096), (70, 33, 4128), (200, 255, 8224), (128, 6, 16384), (520, 700, 2304), (2, 6144, 4096)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
