@@ -101,17 +101,20 @@ struct MxMoeLayout {
     size_t xc = 0, xs = 0, hc = 0, hs = 0, y = 0, total = 0;
 };
 
-// How the layer runs: slot by slot (no routing tables, two launches) while
-// few slots can meet on an expert, else sorted by expert, in row tiles of
-// about twice the mean rows of an expert: 16 or 32 on the streaming kernel,
-// kMxMoeBM on the LDS tiles.
-enum class MoePlan { kSlots, kStream16, kStream32, kTiles };
+// How the layer runs: slot by slot (no sorting, two launches) while few slots
+// can meet on an expert, else sorted by expert, in row tiles of 16 on the
+// streaming kernel or of kMxMoeBM on the LDS tiles.  Measured on MI355X (us,
+// slots / 16 rows / LDS tiles), 256 experts of 6144 x 2048, top 8: 4 tokens 136
+// / 148 / 160, 8 tokens 251 / 245 / 268, 64 tokens 1901 / 886 / 900, 128 tokens
+// - / 1008 / 986, 512 tokens - / 1482 / 1062; 32 experts of 2048 x 1024, top 4:
+// 8 tokens 30 / 32 / 53, 16 tokens 52 / 37 / 58, 128 tokens - / 47 / 61, 256
+// tokens - / 67 / 62.
+enum class MoePlan { kSlots, kStream, kTiles };
 MoePlan plan_mx_moe(const nvfp4_mx_moe_problem& p) {
     const int64_t S = p.T * p.top_k;
-    if (S <= 64 && mx_slots_fit(p.H)) return MoePlan::kSlots;
-    if (S <= 8 * p.E) return MoePlan::kStream16;
-    if (S <= 20 * p.E) return MoePlan::kStream32;
-    return MoePlan::kTiles;
+    if (S <= 32 && mx_slots_fit(p.H)) return MoePlan::kSlots;
+    const bool small = p.E * (p.I * p.H / 2) * 3 < ((int64_t)512 << 20);  // all experts' codes, in bytes
+    return S <= (small ? 16 : 3) * p.E ? MoePlan::kStream : MoePlan::kTiles;
 }
 
 MxMoeLayout layout_mx_moe(const nvfp4_mx_moe_problem& p) {
@@ -155,7 +158,7 @@ int32_t check_mx_moe(const nvfp4_mx_moe_problem* p) {
     // workgroups of the grouped products (256 threads each, fewer than 2^32 in all)
     // (the streaming forms: 512 threads, row tiles of 16, 32 columns of h or 16 of H)
     const int64_t mt = S / kMxMoeBM + p->E + 1, nt = std::max(p->I / 64, p->H / 128) + 1;
-    const int64_t ms = std::min(S, 20 * p->E) / 16 + p->E + 64, ns = std::max(p->I / 32, p->H / 16) + 1;
+    const int64_t ms = std::min(S, 16 * p->E) / 16 + p->E + 64, ns = std::max(p->I / 32, p->H / 16) + 1;
     if (mt * nt >= ((int64_t)1 << 24) || ms * ns >= ((int64_t)1 << 23)) return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_moe: too many tiles");
     return NVFP4_OK;
 }
@@ -343,7 +346,7 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
         if (int32_t e = api_hip(launch_mx_slot_up(up, S, s), "mx_moe gate/up")) return e;
         return api_hip(launch_mx_slot_down(down, p->T, s), "mx_moe down");
     }
-    const int bm = plan == MoePlan::kStream16 ? 16 : plan == MoePlan::kStream32 ? 32 : kMxMoeBM;
+    const int bm = plan == MoePlan::kStream ? 16 : kMxMoeBM;
     int32_t* row_off = at<int32_t>(workspace, l.row_off);
     int32_t* tile_off = at<int32_t>(workspace, l.tile_off);
     int32_t* perm = at<int32_t>(workspace, l.perm);
@@ -368,16 +371,16 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
         if (st) return st;
     }
     const int grid_m = (int)((S + bm - 1) / bm + std::min<int64_t>(E, S));
-    if (plan != MoePlan::kTiles) {
+    if (plan == MoePlan::kStream) {
         up.a_codes = xc;
         up.a_scales = xs;
         up.perm = perm;
         up.row_off = down.row_off = row_off;
         up.tile_off = down.tile_off = tile_off;
         down.y = Y;
-        st = api_hip(launch_mx_group_up(up, bm, grid_m, s), "mx_moe gate/up");
+        st = api_hip(launch_mx_group_up(up, grid_m, s), "mx_moe gate/up");
         if (st) return st;
-        st = api_hip(launch_mx_group_down(down, bm, grid_m, s), "mx_moe down");
+        st = api_hip(launch_mx_group_down(down, grid_m, s), "mx_moe down");
         if (st) return st;
         return api_hip(launch_mx_combine(Y, inv, t->topk_weights, p->T, (int32_t)p->top_k, p->H, t->out, s),
                        "mx_moe combine");

@@ -85,9 +85,9 @@ bool mx_slots_fit(int64_t H);
 hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream);
 hipError_t launch_mx_slot_up(const MxStreamArgs& g, int64_t slots, hipStream_t stream);
 hipError_t launch_mx_slot_down(const MxStreamArgs& g, int64_t tokens, hipStream_t stream);
-// bm (16 or 32): rows of one workgroup; mtiles bounds the row tiles.
-hipError_t launch_mx_group_up(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
-hipError_t launch_mx_group_down(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream);
+// Row tiles of 16; mtiles bounds them.
+hipError_t launch_mx_group_up(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream);
+hipError_t launch_mx_group_down(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream);
 
 // The sorted routed layer's first launch (mx_route.hip): row_off and tile_off
 // [E + 1] (tiles of bm rows), the slot of each expert row perm [slots] and the

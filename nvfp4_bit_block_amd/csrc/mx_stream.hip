@@ -18,8 +18,8 @@
 //   kSlotDown  one workgroup per (token, 16 NR columns): the waves walk the
 //              token's slots in order and weigh them, so the weighted sum
 //              leaves as bf16 without a pass of its own.
-//   kGroupUp, kGroupDown  the same products on expert-sorted rows (up to
-//              16 MB of one expert per workgroup).
+//   kGroupUp, kGroupDown  the same products on expert-sorted rows (up to 16
+//              of one expert per workgroup).
 #include <algorithm>
 #include <type_traits>
 
@@ -486,13 +486,11 @@ hipError_t launch_mx_slot_up(const MxStreamArgs& g, int64_t slots, hipStream_t s
 hipError_t launch_mx_slot_down(const MxStreamArgs& g, int64_t tokens, hipStream_t stream) {
     return launch_k<1, 1, Mode::kSlotDown, false>(g, tokens, stream);
 }
-hipError_t launch_mx_group_up(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream) {
-    return bm == 16 ? launch_k<4, 1, Mode::kGroupUp, false>(g, mtiles, stream)
-                    : launch_k<4, 2, Mode::kGroupUp, false>(g, mtiles, stream);
+hipError_t launch_mx_group_up(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
+    return launch_k<4, 1, Mode::kGroupUp, false>(g, mtiles, stream);
 }
-hipError_t launch_mx_group_down(const MxStreamArgs& g, int bm, int64_t mtiles, hipStream_t stream) {
-    return bm == 16 ? launch_k<4, 1, Mode::kGroupDown, false>(g, mtiles, stream)
-                    : launch_k<2, 2, Mode::kGroupDown, false>(g, mtiles, stream);
+hipError_t launch_mx_group_down(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
+    return launch_k<4, 1, Mode::kGroupDown, false>(g, mtiles, stream);
 }
 
 }  // namespace nvfp4
