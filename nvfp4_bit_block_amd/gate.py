@@ -27,12 +27,6 @@ def _config(T, E, top_k, n_group, topk_group, group_top, score, renormalize, bf1
                          1 if bf16 else 0, scale)
 
 
-def _logits(logits):
-    nv._req(logits, "logits", _LOGITS, (None, None))
-    nv._cuda(logits, "logits")
-    return logits.shape[0], logits.shape[1], logits.device
-
-
 def moe_gate(logits, top_k, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1, group_top=1, renormalize=True,
              scale=1.0, ids=None, weights=None, stream=None):
     """nvfp4_moe_gate: returns (ids int32 [T, top_k], weights fp32 [T, top_k]).
@@ -42,7 +36,7 @@ def moe_gate(logits, top_k, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_grou
     gradient to it).  ``n_group`` runs of experts, of which the ``topk_group``
     with the largest sum of their ``group_top`` best choice values stay.  A
     row with fewer candidates than ``top_k`` ends in ids -1 of weight 0."""
-    T, E, dev = _logits(logits)
+    T, E, dev = nv._matrix(logits, "logits", _LOGITS)
     if bias is not None:
         nv._arg(bias, "bias", nv._F32, (E,), dev)
     c = _config(T, E, top_k, n_group, topk_group, group_top, score, bool(renormalize),
@@ -61,9 +55,11 @@ def moe_gate_backward(logits, ids, dweights, score=SCORE_SOFTMAX, renormalize=Tr
                       stream=None):
     """nvfp4_moe_gate_backward: the gradient of the forward call's weights with
     respect to its logits, [T, E] in their type, at the ids that it chose."""
-    T, E, dev = _logits(logits)
-    nv._req(ids, "ids", nv._I32, (T, None), dev)
-    top_k = ids.shape[1]
+    T, E, dev = nv._matrix(logits, "logits", _LOGITS)
+    rows, top_k, _ = nv._matrix(ids, "ids", nv._I32)
+    if rows != T:
+        raise ValueError(f"ids: {rows} rows, logits has {T}")
+    nv._cuda(ids, "ids", dev)
     nv._arg(dweights, "dweights", nv._F32, (T, top_k), dev)
     c = _config(T, E, top_k, 1, 1, 1, score, bool(renormalize), logits.dtype is torch.bfloat16, float(scale))
 

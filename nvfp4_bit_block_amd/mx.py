@@ -12,20 +12,19 @@ import nvfp4_bit_block_amd as nv
 def _mx_tensor(codes, scales, name, device=None):
     """codes uint8 [R, C/2], scales uint8 [R, C/32], C a multiple of 32, on
     one device (`device` if given); returns (R, C, device)."""
+    # dtypes and shapes first, then the devices
     nv._req(codes, name + "codes", nv._U8, (None, None))
     rows, half = codes.shape
-    nv._req(scales, name + "scales", nv._U8, (rows, half // 16))
     if half % 16:
         raise ValueError(f"{name}codes: rows of {half} bytes are not whole blocks of 32 elements")
-    dev = nv._cuda(codes, name + "codes", device).device
-    nv._cuda(scales, name + "scales", dev)
+    dev = codes.device
+    nv._arg(scales, name + "scales", nv._U8, (rows, half // 16), None if dev.type != "cuda" else dev)
+    nv._cuda(codes, name + "codes", device)
     return rows, 2 * half, dev
 
 
 def _activation(x):
-    nv._bf16(x, "x", (None, None))
-    nv._cuda(x, "x")
-    return x.shape[0], x.shape[1], x.device
+    return nv._matrix(x, "x", nv._BF16)
 
 
 def _mx_weights(w_codes, w_scales, K, dev):

@@ -261,3 +261,82 @@ def test_product_in_a_graph():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, want[i % 2])
+
+
+def test_offsets_past_32_bits():
+    """Operands of more than 2^31 code bytes and 2^32 elements: the last rows
+    equal those of a small call on copies of them."""
+    d = device()
+    g = torch.Generator(device=d).manual_seed(0)
+    rows, cols = (1 << 32) // 4096 + 65, 4096
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=d)
+    x[:1000].normal_(generator=g)
+    x[-1000:].normal_(generator=g)
+    c, s = nv.mx_quantize(x)
+    tc, ts = nv.mx_quantize(x[-1000:].clone())
+    assert torch.equal(c[-1000:], tc) and torch.equal(s[-1000:], ts)
+    assert torch.equal(nv.mx_dequantize(c, s)[-1000:], nv.mx_dequantize(tc, ts))
+    del x
+    w = (torch.randint(0, 256, (40, cols // 2), generator=g, device=d, dtype=torch.uint8),
+         torch.randint(118, 122, (40, cols // 32), generator=g, device=d, dtype=torch.uint8))
+    y = nv.mx_gemm_packed(c, s, *w)                                    # large activation
+    z = nv.mx_gemm_packed(tc, ts, *w)
+    assert (y[-1000:].float() - z.float()).abs().max() <= 2.0 ** -7 * z.float().abs().max()
+    y = nv.mx_gemm_packed(*w, c, s)                                    # large weight
+    z = nv.mx_gemm_packed(*w, tc, ts)
+    assert (y[:, -1000:].float() - z.float()).abs().max() <= 2.0 ** -7 * z.float().abs().max()
+    y = nv.mx_gemm_packed(w[0][:3], w[1][:3], c, s)                    # and through the streaming kernel
+    assert (y[:, -1000:].float() - z[:3].float()).abs().max() <= 2.0 ** -7 * z.float().abs().max()
+
+
+def test_experts_past_32_bits():
+    """A last expert whose weights start past 2 GiB."""
+    d = device()
+    g = torch.Generator(device=d).manual_seed(1)
+    E, H, I = 600, 2048, 2048
+    r = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=d, dtype=torch.uint8)  # noqa: E731
+    w13 = (torch.empty((E, 2 * I, H // 2), dtype=torch.uint8, device=d), r(118, 122, E, 2 * I, H // 32))
+    w2 = (torch.empty((E, H, I // 2), dtype=torch.uint8, device=d), r(118, 122, E, H, I // 32))
+    assert (E - 1) * w13[0][0].numel() > 2 ** 31
+    w13[0][-1], w2[0][-1] = r(0, 256, 2 * I, H // 2), r(0, 256, H, I // 2)
+    for T in (2, 40, 4000):                                            # slots, streamed rows, tiles
+        x = torch.randn((T, H), generator=g, device=d).to(torch.bfloat16)
+        ids = torch.full((T, 1), E - 1, dtype=torch.int32, device=d)
+        tw = torch.ones((T, 1), device=d)
+        y = nv.mx_moe(x, ids, tw, *w13, *w2)
+        z = nv.mx_moe(x, torch.zeros_like(ids), tw, *[t[-1:].clone() for t in (*w13, *w2)])
+        assert (y.float() - z.float()).norm() <= 0.01 * z.float().norm()
+
+
+def test_misaligned_views_are_refused():
+    d = device()
+    c = torch.zeros(4 * 64 + 8, dtype=torch.uint8, device=d)[8:].view(4, 64)
+    s = torch.zeros((4, 4), dtype=torch.uint8, device=d)
+    x = torch.zeros((2, 128), dtype=torch.bfloat16, device=d)
+    for call in (lambda: nv.mx_dequantize(c, s), lambda: nv.mx_gemm(x, c, s)):
+        with pytest.raises(nv.Nvfp4Error, match="aligned"):
+            call()
+    with pytest.raises(ValueError, match="shape"):
+        nv.mx_gemm(x, c.clone(), s, out=torch.empty((2, 5), dtype=torch.bfloat16, device=d))
+    with pytest.raises(nv.Nvfp4Error, match="workspace"):
+        nv.mx_gemm(torch.zeros((70, 128), dtype=torch.bfloat16, device=d), c.clone(), s,
+                   ws=torch.empty(16, dtype=torch.uint8, device=d))
+
+
+def test_two_streams_at_once():
+    """Calls that run together on two streams, each with its own temporaries."""
+    rng = np.random.default_rng(8)
+    case = _experts_case(rng, 90, 8, 3, 256, 128)
+    w = ref.random_mx(rng, 300, 1024)
+    xb = dev_bf16(wl.normal_bf16(rng, (80, 1024), 1.0))
+    W = (dev(w[0]), dev(w[1]))
+    args = [dev_bf16(case[0]), dev(case[1]), dev(case[2]), *map(dev, case[3]), *map(dev, case[4])]
+    want = (nv.mx_moe(*args), nv.mx_gemm(xb, *W))
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        got.append((nv.mx_moe(*args, stream=s1), nv.mx_gemm(xb, *W, stream=s2)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])

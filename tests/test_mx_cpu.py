@@ -205,3 +205,10 @@ def test_lds_loads_of_the_mx_kernels_have_their_wait_states(tmp_path):
     assert re.search(r"buffer_load_\w+\s.*\blds$", asm, re.M)
     bad = hazards(asm)
     assert not bad, bad[:3]
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        nv._launch(torch.device("cuda", 0), Stream(), lambda s: s)
