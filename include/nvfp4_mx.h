@@ -52,9 +52,9 @@ int32_t nvfp4_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t
  * [N, K/2], w_scales [N, K/32]; y bf16 [M, N].
  * nvfp4_mx_gemm: the same on nvfp4_mx_quantize of x bf16 [M, K], quantized
  * within the call.
- * K % 32 == 0 and K > 0 (else SHAPE), any M and N; K < 2^24, M and N <
- * 2^30 and M * N <= 2^36 (else UNSUPPORTED).  Workspace: the sizes below (0: none, and then
- * workspace may be NULL).
+ * K % 32 == 0 and K > 0 (else SHAPE), any M and N; K < 2^24, M < 2^30, N <
+ * 2^28 and M * N <= 2^36 (else UNSUPPORTED).  Workspace: the sizes below (0:
+ * none, and then workspace may be NULL).
  * ------------------------------------------------------------------------ */
 size_t nvfp4_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 int32_t nvfp4_mx_gemm(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,

@@ -48,9 +48,10 @@ int32_t check_gate(const nvfp4_gate_config* c, bool backward) {
 int32_t check_product(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K <= 0 || K % 32 != 0)
         return api_fail(NVFP4_ERR_SHAPE, "mx_gemm: need M, N >= 0, K > 0 and K % 32 == 0");
-    constexpr int64_t kMost = (int64_t)1 << 30;
-    if (K >= ((int64_t)1 << 24) || M >= kMost || N >= kMost || (N > 0 && M > (((int64_t)1 << 36) / N)))
-        return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_gemm: K below 2^24, M and N below 2^30, M * N up to 2^36");
+    // (few rows: a workgroup of 256 threads for 32 or more columns)
+    if (K >= ((int64_t)1 << 24) || M >= ((int64_t)1 << 30) || N >= ((int64_t)1 << 28) ||
+        (N > 0 && M > (((int64_t)1 << 36) / N)))
+        return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_gemm: K below 2^24, M below 2^30, N below 2^28, M * N up to 2^36");
     return NVFP4_OK;
 }
 
@@ -155,11 +156,12 @@ int32_t check_mx_moe(const nvfp4_mx_moe_problem* p) {
     if (p->H >= kBytes || p->I >= kBytes || p->T * (p->H / 2) >= kBytes || S * (p->I / 2) >= kBytes ||
         p->I * p->H >= kBytes)
         return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_moe: an operand of 2 GiB or more");
-    // workgroups of the grouped products (256 threads each, fewer than 2^32 in all)
-    // (the streaming forms: 512 threads, row tiles of 16, 32 columns of h or 16 of H)
+    // workgroups of the grouped products: fewer than 2^32 threads in all (256 each;
+    // the streaming forms: row tiles of 16, 32 columns of h or 16 of H)
     const int64_t mt = S / kMxMoeBM + p->E + 1, nt = std::max(p->I / 64, p->H / 128) + 1;
     const int64_t ms = std::min(S, 16 * p->E) / 16 + p->E + 64, ns = std::max(p->I / 32, p->H / 16) + 1;
-    if (mt * nt >= ((int64_t)1 << 24) || ms * ns >= ((int64_t)1 << 23)) return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_moe: too many tiles");
+    if (mt * nt >= ((int64_t)1 << 24) || ms * ns >= ((int64_t)1 << 23))
+        return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_moe: too many tiles");
     return NVFP4_OK;
 }
 
@@ -252,7 +254,9 @@ int32_t nvfp4_mx_gemm_packed(const uint8_t* a_codes, const uint8_t* a_scales, in
     const size_t need = nvfp4_mx_gemm_packed_workspace_size(M, N, K);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return api_fail(NVFP4_ERR_WORKSPACE, "mx_gemm_packed: workspace smaller than nvfp4_mx_gemm_packed_workspace_size");
-    return api_hip(run_product(a_codes, a_scales, M, N, K, w_codes, w_scales, y, at<float>(workspace, 0), as_stream(stream)), "mx_gemm_packed");
+    return api_hip(run_product(a_codes, a_scales, M, N, K, w_codes, w_scales, y, at<float>(workspace, 0),
+                               as_stream(stream)),
+                   "mx_gemm_packed");
 }
 
 size_t nvfp4_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {

@@ -29,6 +29,7 @@
 #include "mx_internal.hpp"
 #include "nvfp4_dma.hpp"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace nvfp4 {

@@ -21,6 +21,8 @@ def _config(T, E, top_k, n_group, topk_group, group_top, score, renormalize, bf1
     """The C struct of one problem (a pure function of its numbers)."""
     if score not in _SCORES:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    if top_k < 1:
+        raise ValueError(f"top_k must be at least 1, got {top_k}")
     if not (math.isfinite(scale) and scale > 0.0):
         raise ValueError(f"scale must be finite and > 0, got {scale}")
     return nv.GateConfig(T, E, top_k, n_group, topk_group, group_top, _SCORES[score], 1 if renormalize else 0,

@@ -138,6 +138,8 @@ def mx_moe(x, topk_ids, topk_weights, w13_codes, w13_scales, w2_codes, w2_scales
     nv._req(topk_weights, "topk_weights", nv._F32, (T, k))
     nv._req(w13_codes, "w13_codes", nv._U8, (None, None, H // 2))
     E, twoI, _ = w13_codes.shape
+    if twoI % 2:
+        raise ValueError(f"w13_codes: {twoI} rows per expert, need gate and up rows, the same number of each")
     I = twoI // 2
     nv._req(w13_scales, "w13_scales", nv._U8, (E, 2 * I, H // 32))
     nv._req(w2_codes, "w2_codes", nv._U8, (E, H, I // 2))

@@ -340,3 +340,55 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in got:
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+# many experts (bounds searched in two steps), many slots (sorted by several
+# launches), in row tiles of 16 and on the large ones
+MANY = [(40, 4096, 8, 64, 32), (300, 130, 8, 96, 64), (1100, 600, 8, 64, 32), (2100, 20, 4, 160, 96)]
+
+
+@pytest.mark.parametrize("T,E,k,H,I", MANY)
+def test_experts_many(T, E, k, H, I):
+    rng = np.random.default_rng(T + E)
+    case = _experts_case(rng, T, E, k, H, I, skip=0.1)
+    _check_experts(_run_experts(*case), *case)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [MANY[1], MANY[3]])
+def test_experts_in_a_graph(T, E, k, H, I):
+    """Replays with other tokens and other routing, eager work between them."""
+    rng = np.random.default_rng(T)
+    x, ids, tw, w13, w2 = _experts_case(rng, T, E, k, H, I)
+    x2, ids2 = wl.normal_bf16(rng, (T, H), 1.0), np.full_like(ids, 1)
+    W = (dev(w13[0]), dev(w13[1]), dev(w2[0]), dev(w2[1]))
+    xs, idss, twd = [dev_bf16(x), dev_bf16(x2)], [dev(ids), dev(ids2)], dev(tw)
+    want = [nv.mx_moe(xs[i], idss[i], twd, *W) for i in range(2)]
+    xd, idd = xs[0].clone(), idss[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = nv.mx_moe(xd, idd, twd, *W)
+    for i in range(4):
+        xd.copy_(xs[i % 2])
+        idd.copy_(idss[i % 2])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i % 2])
+        assert torch.equal(nv.mx_moe(xs[1], idss[1], twd, *W), want[1])
+
+
+@pytest.mark.parametrize("T", [2, 40, 200])
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80, 0xFF80])
+def test_a_token_that_is_not_finite_stays_by_itself(T, bad):
+    rng = np.random.default_rng(T)
+    x, ids, tw, w13, w2 = _experts_case(rng, T, 4, 2, 128, 64)
+    clean = host_bf16_f32(_run_experts(x, ids, tw, w13, w2))
+    p = dev_bf16(x)
+    W = (dev(w2[0][0]), dev(w2[1][0]))                            # [128, 64]: takes 64 columns
+    product = host_bf16_f32(nv.mx_gemm(p[:, :64].contiguous(), *W))
+    xb = x.copy()
+    xb[1, 5] = bad
+    y = host_bf16_f32(_run_experts(xb, ids, tw, w13, w2))
+    z = host_bf16_f32(nv.mx_gemm(dev_bf16(xb)[:, :64].contiguous(), *W))
+    rest = np.arange(T) != 1
+    assert np.array_equal(y[rest], clean[rest]) and np.isnan(y[1]).all()
+    assert np.array_equal(z[rest], product[rest]) and np.isnan(z[1]).all()

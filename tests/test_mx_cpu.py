@@ -212,3 +212,26 @@ def test_a_stream_of_another_device_is_refused():
         device = torch.device("cuda", 1)
     with pytest.raises(ValueError, match="stream of cuda:1"):
         nv._launch(torch.device("cuda", 0), Stream(), lambda s: s)
+
+
+def test_binding_refuses_an_odd_number_of_gate_up_rows():
+    x, ids, w = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))
+    def u8(*shape):
+        return torch.zeros(shape, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="gate and up"):
+        nv.mx_moe(x, ids, w, u8(3, 65, 32), u8(3, 64, 2), u8(3, 64, 16), u8(3, 64, 1))
+
+
+def test_binding_refuses_a_top_k_below_one():
+    from nvfp4_bit_block_amd import gate
+    for top_k in (0, -1):
+        with pytest.raises(ValueError, match="top_k"):
+            gate._config(4, 16, top_k, 1, 1, 1, "softmax", True, False, 1.0)
+
+
+def test_product_limits():
+    """One launch holds fewer than 2^32 threads: N of 2^28 and more is refused."""
+    L = nv.lib()
+    for N in (1 << 28, (1 << 30) - 1):
+        assert L.nvfp4_mx_gemm(A, 1, N, 32, A, A, A, A, 1 << 40, None) == UNSUP
+        assert L.nvfp4_mx_gemm_packed(A, A, 1, N, 32, A, A, A, A, 1 << 40, None) == UNSUP
