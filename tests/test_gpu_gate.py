@@ -223,3 +223,17 @@ def test_gate_leaves_other_memory_alone():
     assert (d[5:] == 7.0).all()
     empty = nv.moe_gate(x[:0], 6)
     assert empty[0].shape == (0, 6)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k,G,kg,group_top,score,renorm", [
+    (2049, 7, 3, 1, 1, 1, "softmax", False), (2051, 60, 6, 5, 2, 2, "sigmoid", True),
+    (2050, 128, 16, 128, 20, 1, "softmax", True), (3001, 256, 8, 8, 4, 2, "sigmoid", True),
+    (2049, 256, 8, 1, 1, 1, "softmax", False), (2049, 250, 16, 2, 1, 1, "sigmoid", False)])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_gate_many_tokens(dtype, T, E, k, G, kg, group_top, score, renorm, with_bias):
+    """Four tokens to a wave."""
+    rng = np.random.default_rng(T + E + k + G)
+    bias = torch.from_numpy(rng.standard_normal(E).astype(np.float32) * np.float32(0.2)) if with_bias else None
+    l, l64 = _logits(rng, T, E, dtype, masked=True)
+    _check(l, l64, k, score=score, renormalize=renorm, bias=bias, n_group=G, topk_group=kg, group_top=group_top)
