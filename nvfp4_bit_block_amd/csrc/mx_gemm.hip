@@ -375,6 +375,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     if (TM >= 2 && used == 1) main_loop(std::integral_constant<int, 1>{});
     else if (TM >= 3 && used == 2) main_loop(std::integral_constant<int, TM >= 3 ? 2 : TM>{});
     else if (TM >= 4 && used == 3) main_loop(std::integral_constant<int, TM >= 4 ? 3 : TM>{});
+    else if (TM >= 5 && used == 4) main_loop(std::integral_constant<int, TM >= 5 ? 4 : TM>{});
+    else if (TM >= 6 && used == 5) main_loop(std::integral_constant<int, TM >= 6 ? 5 : TM>{});
     else main_loop(std::integral_constant<int, TM>{});
     __builtin_amdgcn_s_waitcnt(kWaitAll);
 
@@ -541,10 +543,15 @@ hipError_t launch_mx_gemm_split(const MxGemmArgs& g0, float* partial, hipStream_
 //   4096 x 16384 x 2048     2172        3000        2668
 // The large tiles need one workgroup per CU and few partly filled rounds; on
 // short rows 256 x 192's odd tile count and longer tail lose.
+// Grouped: 192 x 256, each wave all the rows and 64 weight rows, so that the
+// main loop counts an expert's rows by 32.  Gate/up and down of 256 experts of
+// 6144 x 2048, top 8 (us; 2 x 2 waves, which count them by 64, in brackets):
+// 4096 tokens 831 and 486 (846, 486), 2560 738 and 415 (752, 426), 640 648 and
+// 368 (659, 375).
 hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream) {
     if (g.groups > 0)
-        return epi == MxEpi::kGateUp ? launch_cfg<3, 4, 2, 2, 3, 2, MxEpi::kGateUp>(g, grid_m, stream)
-                                     : launch_cfg<3, 4, 2, 2, 3, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
+        return epi == MxEpi::kGateUp ? launch_cfg<6, 2, 1, 4, 3, 2, MxEpi::kGateUp>(g, grid_m, stream)
+                                     : launch_cfg<6, 2, 1, 4, 3, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
     // share of the CUs' time that a tile's rounds fill
     auto fill = [&](int64_t bm, int64_t bn, int64_t slots) {
         const int64_t t = ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn);
