@@ -21,10 +21,10 @@
 //   kGroupUp, kGroupDown  the same products on expert-sorted rows (up to 16
 //              of one expert per workgroup).
 #include <algorithm>
-#include <type_traits>
 
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
+#include "nvfp4_dma.hpp"
 
 namespace nvfp4 {
 
@@ -37,11 +37,17 @@ constexpr int waves_of(int nr) { return nr == 4 ? 4 : 8; }
 // Waves per SIMD that the registers allow.
 constexpr int wpe_of(int nr, int mb) { return nr * mb <= 2 ? 4 : nr * mb <= 4 ? 2 : 1; }
 
-// One operand's rows as a lane sees them: the lane's row offset (bytes) into
-// codes and scales, from uniform bases.
-struct RowPtr {
+// One operand: uniform bases of codes and scales and the bytes that are
+// reached from them, all below 2 GiB.
+struct Rows {
     const uint8_t* codes;
     const uint8_t* scales;
+    uint32_t code_bytes, scale_bytes;
+};
+// A row of it as a lane sees it: offsets of its piece of the codes and of the
+// row's scales.
+struct RowAt {
+    uint32_t c, s;
 };
 
 // codes and scale words of one 128-element step for this lane.
@@ -51,44 +57,67 @@ struct Step {
 };
 
 // A unit of K: USTEPS steps of 128 elements whose scale bytes of a row are
-// one aligned load (4: 16 bytes, 2: 8 bytes); 1: K is no multiple of 256, the
-// scale bytes are loaded one by one and blocks past K read as zeros.
+// one aligned load (4: 16 bytes, 2: 8 bytes); 1: K is no multiple of 256 and
+// the scale bytes are loaded one by one.
 template <int USTEPS>
 struct Unit {
     Step st[USTEPS];
 };
 
-// (Plain loads, not non-temporal ones: an instruction reads half a cache line
-// of each row and the next one the other half, which a line that is not kept
-// fetches again: 28.1 against 18.9 us for one token's gate/up product of 8
-// experts, 6144 x 2048.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)bytes, (int)kRsrcWord3);
+}
+
+// A unit that is not live, and blocks past K, are pushed out of range: they
+// read as zeros, without a memory access.  (Loads that keep their lines, not
+// non-temporal ones: an instruction reads half a cache line of each row and
+// the next one the other half, which a line that is not kept fetches again:
+// 28.1 against 18.9 us for one token's gate/up product of 8 experts, 6144 x
+// 2048.)
 template <int USTEPS>
-__device__ __forceinline__ Unit<USTEPS> load_unit(const RowPtr& r, int unit, int g, int nblk) {
+__device__ __forceinline__ Unit<USTEPS> load_unit(const Rows& r, const RowAt& at, int unit, bool live, int g, int nblk) {
     Unit<USTEPS> u;
+    const auto rc = buffer(r.codes, r.code_bytes), rs = buffer(r.scales, r.scale_bytes);
     if constexpr (USTEPS > 1) {
-        const uint8_t* c = r.codes + (size_t)unit * (64 * USTEPS) + 16 * g;
+        const uint32_t dead = live ? 0u : kOob;
+        const int vc = (int)(at.c | dead), vs = (int)(at.s | dead);
 #pragma unroll
         for (int i = 0; i < USTEPS; ++i)
-            u.st[i].c = *reinterpret_cast<const u32x4*>(c + 64 * i);
-        uint32_t s[4];
+            u.st[i].c = __builtin_amdgcn_raw_buffer_load_b128(rc, vc + 64 * i, unit * (64 * USTEPS), 0);
         if constexpr (USTEPS == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(r.scales + (size_t)unit * 16);
-            s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(r.scales + (size_t)unit * 8);
-            s[0] = v.x, s[1] = v.y;
-        }
-        // (this lane's byte is shifted down where it is used, so that the
-        // load need not be waited for here)
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, vs, unit * 16, 0);
 #pragma unroll
-        for (int i = 0; i < USTEPS; ++i) u.st[i].s = s[i];
+            for (int i = 0; i < 4; ++i) u.st[i].s = v[i];
+        } else {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, vs, unit * 8, 0);
+            u.st[0].s = v[0];
+            u.st[1].s = v[1];
+        }
+    } else {
+        const uint32_t dead = live && 4 * unit + g < nblk ? 0u : kOob;
+        u.st[0].c = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(at.c | dead), unit * 64, 0);
+        u.st[0].s = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)((at.s + g) | dead), unit * 4, 0);
+    }
+    return u;
+}
+// The same of an activation in LDS (a live unit).
+template <int USTEPS>
+__device__ __forceinline__ Unit<USTEPS> lds_unit(const uint8_t* codes, const uint8_t* scales, int unit, int g, int nblk) {
+    Unit<USTEPS> u;
+    if constexpr (USTEPS > 1) {
+        const uint8_t* c = codes + unit * (64 * USTEPS) + 16 * g;
+#pragma unroll
+        for (int i = 0; i < USTEPS; ++i) {
+            u.st[i].c = *reinterpret_cast<const u32x4*>(c + 64 * i);
+            u.st[i].s = *reinterpret_cast<const uint32_t*>(scales + unit * (4 * USTEPS) + 4 * i);
+        }
     } else {
         const int b = 4 * unit + g;
         u.st[0].c = u32x4{0, 0, 0, 0};
         u.st[0].s = 0;
         if (b < nblk) {
-            u.st[0].c = *reinterpret_cast<const u32x4*>(r.codes + (size_t)b * 16);
-            u.st[0].s = r.scales[b];
+            u.st[0].c = *reinterpret_cast<const u32x4*>(codes + b * 16);
+            u.st[0].s = scales[b];
         }
     }
     return u;
@@ -107,11 +136,12 @@ struct SliceItem {
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = p[q];
     }
-    __device__ __forceinline__ void store(uint8_t* lc, uint8_t* ls, int cap, int blocks, int i) const {
+    __device__ __forceinline__ void store(uint8_t* lc, uint8_t* ls, int cap, int blocks, int i) {
         const int m = i / blocks, b = i - m * blocks;
         uint32_t mx = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+            asm("" : "+v"(v[q].x), "+v"(v[q].y), "+v"(v[q].z), "+v"(v[q].w));  // (opaque until here, as in Stream)
             mx = max_bf16x2(mx, v[q].x);
             mx = max_bf16x2(mx, v[q].y);
             mx = max_bf16x2(mx, v[q].z);
@@ -127,55 +157,73 @@ struct SliceItem {
     }
 };
 
-// The weights (and packed activations) of UC units in flight.
-template <int NR, int MB, int USTEPS, int UC, bool A_LDS>
+// D units in flight: their weights, and the packed activations (A_LDS: these
+// are in LDS, and read when they are used).
+//
+// The compiler counts the loads in flight where it needs one of them, but past
+// a branch around a load it cannot, and waits for all; and it moves arithmetic
+// on a loaded word up to the load, and waits there.  So no load is branched
+// around, and the scale words are opaque until they are used.
+template <int NR, int MB, int USTEPS, int D, bool A_LDS>
 struct Stream {
-    Unit<USTEPS> w[2][UC][NR];
-    Unit<USTEPS> a[A_LDS ? 1 : 2][A_LDS ? 1 : UC][A_LDS ? 1 : MB];
+    Rows wr, ar;                // weights, activations
+    RowAt w_at[NR], a_at[MB];
+    const uint8_t* a_codes;     // A_LDS: the row in LDS, from unit 0
+    const uint8_t* a_scales;
+    Unit<USTEPS> w[D][NR];
+    Unit<USTEPS> a[A_LDS ? 1 : D][A_LDS ? 1 : MB];
 
-    __device__ __forceinline__ void fetch(const RowPtr (&wp)[NR], const RowPtr (&ap)[MB], int u, int u1, int buf, int g,
-                                          int nblk) {
+    __device__ __forceinline__ void fetch(int u, int u1, int slot, int g, int nblk) {
+        __builtin_amdgcn_sched_barrier(0);
+        const bool live = u < u1;
 #pragma unroll
-        for (int c = 0; c < UC; ++c)
-            if (u + c < u1) {
+        for (int i = 0; i < NR; ++i) w[slot][i] = load_unit<USTEPS>(wr, w_at[i], u, live, g, nblk);
+        if constexpr (!A_LDS)
 #pragma unroll
-                for (int i = 0; i < NR; ++i) w[buf][c][i] = load_unit<USTEPS>(wp[i], u + c, g, nblk);
-                if constexpr (!A_LDS)
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) a[buf][c][m] = load_unit<USTEPS>(ap[m], u + c, g, nblk);
-            }
+            for (int m = 0; m < MB; ++m) a[slot][m] = load_unit<USTEPS>(ar, a_at[m], u, live, g, nblk);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    __device__ __forceinline__ void use(f32x4 (&acc)[NR][MB], const RowPtr (&ap)[MB], int u, int u1, int buf, int g,
-                                        int nblk) {
-        const int sh = USTEPS > 1 ? 8 * g : 0;
+    __device__ __forceinline__ void start(int u0, int u1, int g, int nblk) {
 #pragma unroll
-        for (int c = 0; c < UC; ++c) {
-            if (u + c >= u1) break;
-            Unit<USTEPS> av[MB];
+        for (int c = 0; c < D; ++c) fetch(u0 + c, u1, c, g, nblk);
+    }
+    __device__ __forceinline__ void use(f32x4 (&acc)[NR][MB], int u, int slot, int g, int nblk) {
+        auto scale = [&](uint32_t s) -> uint32_t {
+            asm("" : "+v"(s));
+            return USTEPS > 1 ? s >> (8 * g) : s;
+        };
+        Unit<USTEPS> av[MB];
 #pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                if constexpr (A_LDS) av[m] = load_unit<USTEPS>(ap[m], u + c, g, nblk);
-                else av[m] = a[buf][c][m];
+        for (int m = 0; m < MB; ++m) {
+            if constexpr (A_LDS) av[m] = lds_unit<USTEPS>(a_codes, a_scales, u, g, nblk);
+            else av[m] = a[slot][m];
+        }
+#pragma unroll
+        for (int s = 0; s < USTEPS; ++s) {
+            uint32_t sa[MB];
+#pragma unroll
+            for (int m = 0; m < MB; ++m) sa[m] = scale(av[m].st[s].s);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const uint32_t sw = scale(w[slot][i].st[s].s);
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+                    acc[i][m] = mx_mfma16<0, 0>(w[slot][i].st[s].c, av[m].st[s].c, acc[i][m], sw, sa[m]);
             }
-#pragma unroll
-            for (int s = 0; s < USTEPS; ++s)
-#pragma unroll
-                for (int i = 0; i < NR; ++i)
-#pragma unroll
-                    for (int m = 0; m < MB; ++m)
-                        acc[i][m] = mx_mfma16<0, 0>(w[buf][c][i].st[s].c, av[m].st[s].c, acc[i][m],
-                                                    w[buf][c][i].st[s].s >> sh, av[m].st[s].s >> sh);
         }
     }
-    // acc += W A^T over units [u0, u1), the first 2 UC of which are in flight
-    __device__ __forceinline__ void run(f32x4 (&acc)[NR][MB], const RowPtr (&wp)[NR], const RowPtr (&ap)[MB], int u0,
-                                        int u1, int g, int nblk) {
-        for (int u = u0; u < u1; u += 2 * UC) {
-            use(acc, ap, u, u1, 0, g, nblk);
-            fetch(wp, ap, u + 2 * UC, u1, 0, g, nblk);
-            use(acc, ap, u + UC, u1, 1, g, nblk);
-            fetch(wp, ap, u + 3 * UC, u1, 1, g, nblk);
-        }
+    // acc += W A^T over units [u0, u1), the first D of which start() asked for
+    __device__ __forceinline__ void run(f32x4 (&acc)[NR][MB], int u0, int u1, int g, int nblk) {
+        int u = u0;
+        for (; u + D < u1; u += D)
+#pragma unroll
+            for (int c = 0; c < D; ++c) {
+                use(acc, u + c, c, g, nblk);
+                fetch(u + c + D, u1, c, g, nblk);
+            }
+#pragma unroll
+        for (int c = 0; c < D; ++c)
+            if (u + c < u1) use(acc, u + c, c, g, nblk);
     }
 };
 
@@ -184,18 +232,13 @@ enum class Mode : int { kPlain = 0, kSlotUp = 1, kSlotDown = 2, kGroupUp = 3, kG
 // QUANT: the activation is bf16 and each wave quantizes its K slice into
 // LDS (kPlain: up to 16 rows; kSlotUp).  The LDS of a wave: `slice` blocks
 // per row.
-template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT>
+template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT, int D>
 __global__ __launch_bounds__(64 * waves_of(NR)) __attribute__((amdgpu_waves_per_eu(wpe_of(NR, MB))))
 void k_mx_stream(MxStreamArgs g) {
     constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
     constexpr bool kUp = MODE == Mode::kSlotUp || MODE == Mode::kGroupUp;
     static_assert(!kUp || NR == 4, "gate/up: two tiles each");
-    // units in flight, twice: 8 code loads a lane of weights alone, 8 of both
-    // operands
-    constexpr int kSteps = QUANT ? 8 : MB == 1 ? 4 : 2;
-    constexpr int UC = USTEPS * NR >= kSteps ? 1 : kSteps / (USTEPS * NR);
-    using S = Stream<NR, MB, USTEPS, UC, QUANT>;
-    S st;
+    Stream<NR, MB, USTEPS, D, QUANT> st;
     extern __shared__ __align__(16) uint8_t smem[];
     float* const red = reinterpret_cast<float*>(smem);  // [wave][tile][lane][4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -237,10 +280,15 @@ void k_mx_stream(MxStreamArgs g) {
     // weight rows of tile i, of which the first rt are the tile's (see
     // rows_per_tile); others, and rows past N, repeat one and are never stored
     const int rt = kUp ? 16 : g.rt;
-    auto w_row = [&](int i) -> int64_t {
-        if constexpr (kUp) return (i < 2 ? 0 : half) + n0 + 16 * (i & 1) + l16;
-        const int64_t n = n0 + rt * i + min(l16, rt - 1);
-        return n < g.N ? n : g.N - 1;
+    auto w_row = [&](int i) -> uint32_t {  // from n0 on
+        if constexpr (kUp) return (uint32_t)(i < 2 ? 0 : half) + 16 * (i & 1) + l16;
+        return (uint32_t)min((int64_t)(rt * i + min(l16, rt - 1)), g.N - 1 - n0);
+    };
+    auto weights = [&](int64_t e) {
+        const int64_t r0 = e * g.N + n0, rows = kUp ? half + 32 : min((int64_t)(16 * NR), g.N - n0);
+        st.wr = {g.b_codes + r0 * KB, g.b_scales + r0 * KS, (uint32_t)(rows * KB), (uint32_t)(rows * KS)};
+#pragma unroll
+        for (int i = 0; i < NR; ++i) st.w_at[i] = {w_row(i) * (uint32_t)KB + 16u * lg, w_row(i) * (uint32_t)KS};
     };
 
     f32x4 acc[NR][MB];
@@ -261,19 +309,14 @@ void k_mx_stream(MxStreamArgs g) {
             const int32_t e = g.ids[s];
             if (e < 0 || e >= g.E) continue;
             const float wj = g.slot_w[s];
-            RowPtr w[NR], a[1];
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const int64_t r = (int64_t)e * g.N + w_row(i);
-                w[i] = {g.b_codes + r * KB, g.b_scales + r * KS};
-            }
-            a[0] = {g.a_codes + s * KB, g.a_scales + s * KS};
+            weights(e);
+            st.ar = {g.a_codes + s * KB, g.a_scales + s * KS, (uint32_t)KB, (uint32_t)KS};
+            st.a_at[0] = {16u * lg, 0u};
             f32x4 part[NR][1];
 #pragma unroll
             for (int i = 0; i < NR; ++i) part[i][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            st.fetch(w, a, u0, u1, 0, lg, nblk);
-            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
-            st.run(part, w, a, u0, u1, lg, nblk);
+            st.start(u0, u1, lg, nblk);
+            st.run(part, u0, u1, lg, nblk);
 #pragma unroll
             for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -281,12 +324,7 @@ void k_mx_stream(MxStreamArgs g) {
         }
     } else {
         const int u0 = wave * units / kWaves, u1 = (wave + 1) * units / kWaves;
-        RowPtr w[NR], a[MB];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const int64_t r = expert * g.N + w_row(i);
-            w[i] = {g.b_codes + r * KB, g.b_scales + r * KS};
-        }
+        weights(expert);
         if constexpr (QUANT) {
             // this wave's slice of every row, quantized into its own LDS; the
             // operand reads below see it through pointers that start at unit 0
@@ -300,15 +338,15 @@ void k_mx_stream(MxStreamArgs g) {
             const int items = rows * blocks;
             SliceItem first;
             if (lane < items) first.load(x, g.K, b0, blocks, lane);
-            st.fetch(w, a, u0, u1, 0, lg, nblk);
-            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
+            st.start(u0, u1, lg, nblk);
             if (lane < items) first.store(lc, ls, cap, blocks, lane);
             for (int i = lane + 64; i < items; i += 64) {
                 first.load(x, g.K, b0, blocks, i);
                 first.store(lc, ls, cap, blocks, i);
             }
             const int mr = l16 < rows ? l16 : 0;
-            a[0] = {lc + ((size_t)mr * cap - b0) * 16, ls + (size_t)mr * cap - b0};
+            st.a_codes = lc + (mr * cap - b0) * 16;
+            st.a_scales = ls + mr * cap - b0;
             __builtin_amdgcn_wave_barrier();
         } else {
 #pragma unroll
@@ -316,12 +354,12 @@ void k_mx_stream(MxStreamArgs g) {
                 int64_t r = row_beg + 16 * m + l16;
                 if (r >= row_end) r = row_beg;
                 if constexpr (MODE == Mode::kGroupUp) r = g.perm[r] / g.top_k;
-                a[m] = {g.a_codes + r * KB, g.a_scales + r * KS};
+                st.a_at[m] = {(uint32_t)(r * KB) + 16u * lg, (uint32_t)(r * KS)};
             }
-            st.fetch(w, a, u0, u1, 0, lg, nblk);
-            st.fetch(w, a, u0 + UC, u1, 1, lg, nblk);
+            st.ar = {g.a_codes, g.a_scales, kOob, kOob};  // (rows below 2 GiB, all of them there)
+            st.start(u0, u1, lg, nblk);
         }
-        st.run(acc, w, a, u0, u1, lg, nblk);
+        st.run(acc, u0, u1, lg, nblk);
         if constexpr (QUANT) __syncthreads();  // the sums below reuse the slices' LDS
     }
 
@@ -405,6 +443,14 @@ int rows_per_tile(int64_t N, int nr) {
     return rt;
 }
 
+// Units in flight: 16 code loads a lane of weights alone, 8 and their
+// activation's (4 where the scale bytes come one by one); at least two units.
+template <int NR, int MB, int USTEPS, bool QUANT>
+constexpr int units_in_flight() {
+    constexpr int steps = USTEPS == 1 ? 2 : QUANT ? 16 : MB == 1 ? 8 : 4;
+    return std::max(2, steps / (USTEPS * NR));
+}
+
 template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT>
 hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
     constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
@@ -419,7 +465,14 @@ hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
         lds = std::max(lds, (size_t)kWaves * (MODE == Mode::kPlain ? (size_t)g.M : 1) * g.slice * 17);
     }
     if (lds > 64 * 1024) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
+    // (units past a wave's last cost an issue each: two where it has no more;
+    // 1 x 6144 x 2080 7.2 -> XX us)
+    constexpr int D = units_in_flight<NR, MB, USTEPS, QUANT>();
+    const bool few = MODE != Mode::kSlotDown && g.K <= (int64_t)2 * kWaves * 128 * USTEPS;
+    if (few)
+        hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, 2>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
+    else
+        hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, D>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
     return hipGetLastError();
 }
 
