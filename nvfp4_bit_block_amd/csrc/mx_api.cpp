@@ -105,17 +105,28 @@ struct MxMoeLayout {
 // How the layer runs: slot by slot (no sorting, two launches) while few slots
 // can meet on an expert, else sorted by expert, in row tiles of 16 on the
 // streaming kernel or of kMxMoeBM on the LDS tiles.  Measured on MI355X (us,
-// slots / 16 rows / LDS tiles), 256 experts of 6144 x 2048, top 8: 4 tokens 136
-// / 148 / 160, 8 tokens 251 / 245 / 268, 64 tokens 1901 / 886 / 900, 128 tokens
-// - / 1008 / 986, 512 tokens - / 1482 / 1062; 32 experts of 2048 x 1024, top 4:
-// 8 tokens 30 / 32 / 53, 16 tokens 52 / 37 / 58, 128 tokens - / 47 / 61, 256
-// tokens - / 67 / 62.
+// slots / 16 rows / LDS tiles), E experts of H x I, uniform routing:
+//   E = 256, 6144 x 2048, top 8   4 tokens 133 / 136 / 152, 8: 257 / 248 / 268,
+//     64: 1954 / 850 / 847, 128: - / 982 / 971, 512: - / 1424 / 1035
+//   256, 2048 x 1024, top 8       8: 44 / 52 / 77, 16: 88 / 90 / 125,
+//     256: - / 201 / 225, 512: - / 275 / 232
+//   64, 2048 x 1408, top 6        4: 29 / 33 / 57, 8: 47 / 47 / 79,
+//     128: - / 79 / 100, 256: - / 122 / 105
+//   32, 2048 x 1024, top 4        8: 31 / 30 / 52, 128: - / 56 / 61,
+//     256: - / 65 / 62
+//   8, 4096 x 2048, top 2         4: 28 / 33 / 50, 8: 46 / 35 / 68,
+//     64: - / 43 / 56, 128: - / 64 / 56
 enum class MoePlan { kSlots, kStream, kTiles };
 MoePlan plan_mx_moe(const nvfp4_mx_moe_problem& p) {
-    const int64_t S = p.T * p.top_k;
-    if (S <= 32 && mx_slots_fit(p.H)) return MoePlan::kSlots;
-    const bool small = p.E * (p.I * p.H / 2) * 3 < ((int64_t)512 << 20);  // all experts' codes, in bytes
-    return S <= (small ? 16 : 3) * p.E ? MoePlan::kStream : MoePlan::kTiles;
+    const int64_t S = p.T * p.top_k, expert = p.I * p.H / 2 * 3;  // an expert's codes, in bytes
+    // Two slots of different tokens share an expert about S (S - top_k) / 2E
+    // times, and its second reading costs more than sorting does from about 55 MB
+    // on.
+    if (S <= 128 && mx_slots_fit(p.H) && S * (S - p.top_k) * expert <= p.E * 110000000) return MoePlan::kSlots;
+    // Beyond 16 rows the streaming kernel reads an expert again, out of the
+    // caches while all of them are small.
+    return S <= p.E * std::min<int64_t>(24, 3 + ((int64_t)1 << 32) / (p.E * expert)) ? MoePlan::kStream
+                                                                                    : MoePlan::kTiles;
 }
 
 MxMoeLayout layout_mx_moe(const nvfp4_mx_moe_problem& p) {

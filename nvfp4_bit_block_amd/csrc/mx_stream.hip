@@ -34,8 +34,9 @@ namespace {
 // more than 128 registers, so that several workgroups share a CU (one loads
 // while another adds up).
 constexpr int waves_of(int nr) { return nr == 4 ? 4 : 8; }
-// Waves per SIMD that the registers allow.
-constexpr int wpe_of(int nr, int mb) { return nr * mb <= 2 ? 4 : nr * mb <= 4 ? 2 : 1; }
+// Waves per SIMD: four, or three where a wave has four tiles (64 tokens, 8 of
+// 256 experts, 6144 x 2048: 814 us, where two take 853 and four 888).
+constexpr int wpe_of(int nr, int mb) { return nr * mb <= 2 ? 4 : 3; }
 
 // One operand: uniform bases of codes and scales and the bytes that are
 // reached from them, all below 2 GiB.
@@ -69,17 +70,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint3
 }
 
 // A unit that is not live, and blocks past K, are pushed out of range: they
-// read as zeros, without a memory access.  (Loads that keep their lines, not
-// non-temporal ones: an instruction reads half a cache line of each row and
-// the next one the other half, which a line that is not kept fetches again:
-// 28.1 against 18.9 us for one token's gate/up product of 8 experts, 6144 x
-// 2048.)
+// read as zeros, without a memory access.  (The scalar offset stays inside the
+// buffer, so that the range check holds whichever way it counts it.)  Loads
+// that keep their lines, not non-temporal ones: an instruction reads half a
+// cache line of each row and the next one the other half, which a line that is
+// not kept fetches again (28.1 against 18.9 us for one token's gate/up product
+// of 8 experts, 6144 x 2048).
 template <int USTEPS>
 __device__ __forceinline__ Unit<USTEPS> load_unit(const Rows& r, const RowAt& at, int unit, bool live, int g, int nblk) {
     Unit<USTEPS> u;
     const auto rc = buffer(r.codes, r.code_bytes), rs = buffer(r.scales, r.scale_bytes);
     if constexpr (USTEPS > 1) {
         const uint32_t dead = live ? 0u : kOob;
+        unit = live ? unit : 0;
         const int vc = (int)(at.c | dead), vs = (int)(at.s | dead);
 #pragma unroll
         for (int i = 0; i < USTEPS; ++i)
@@ -95,6 +98,7 @@ __device__ __forceinline__ Unit<USTEPS> load_unit(const Rows& r, const RowAt& at
         }
     } else {
         const uint32_t dead = live && 4 * unit + g < nblk ? 0u : kOob;
+        unit = live ? unit : 0;
         u.st[0].c = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(at.c | dead), unit * 64, 0);
         u.st[0].s = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)((at.s + g) | dead), unit * 4, 0);
     }
@@ -465,14 +469,16 @@ hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
         lds = std::max(lds, (size_t)kWaves * (MODE == Mode::kPlain ? (size_t)g.M : 1) * g.slice * 17);
     }
     if (lds > 64 * 1024) return hipErrorInvalidValue;
-    // (units past a wave's last cost an issue each: two where it has no more;
-    // 1 x 6144 x 2080 7.2 -> XX us)
+    // (a unit past a wave's last still issues its loads: two where it has no
+    // more; 37 x 4099 x 2080 with four 11.5, with two 9.6 us)
     constexpr int D = units_in_flight<NR, MB, USTEPS, QUANT>();
-    const bool few = MODE != Mode::kSlotDown && g.K <= (int64_t)2 * kWaves * 128 * USTEPS;
-    if (few)
-        hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, 2>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
-    else
-        hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, D>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
+    if constexpr (MODE == Mode::kPlain && D > 2)
+        if (g.K <= (int64_t)2 * kWaves * 128 * USTEPS) {
+            hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, 2>), dim3((unsigned)wgs), dim3(kThreads), lds,
+                               stream, g);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, D>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
     return hipGetLastError();
 }
 

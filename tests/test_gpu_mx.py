@@ -392,3 +392,20 @@ def test_a_token_that_is_not_finite_stays_by_itself(T, bad):
     rest = np.arange(T) != 1
     assert np.array_equal(y[rest], clean[rest]) and np.isnan(y[1]).all()
     assert np.array_equal(z[rest], product[rest]) and np.isnan(z[1]).all()
+
+
+# the streaming kernel's forms: one, two and four weight tiles a wave, one, two
+# and four activation tiles, short and long rows, whole and odd blocks
+@pytest.mark.parametrize("M,N,K", [(1, 70, 16384), (2, 70, 12288), (1, 70, 8448), (1, 70, 8480), (3, 70, 8448), (4, 33, 8224),
+                                   (1, 8200, 4352), (2, 8209, 160), (3, 8200, 4352), (1, 16500, 544), (1, 16400, 512),
+                                   (20, 100, 2304), (20, 8200, 256), (20, 8200, 96), (40, 130, 1280), (64, 65, 2080)])
+def test_product_streaming(M, N, K):
+    test_product(M, N, K)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(16, 256, 8, 64, 32), (7, 40, 9, 96, 64), (10, 300, 10, 256, 160), (2, 8, 2, 544, 352),
+                                       (1, 200, 128, 64, 32), (1, 200, 129, 64, 32)])
+def test_experts_slot_by_slot(T, E, k, H, I):
+    rng = np.random.default_rng(T * E + k)
+    case = _experts_case(rng, T, E, k, H, I, skip=0.1)
+    _check_experts(_run_experts(*case), *case)
