@@ -485,7 +485,7 @@ hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
 template <int NR, int MB, Mode MODE, bool QUANT>
 hipError_t launch_k(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
     // units of four steps where one tile's waves then share them evenly
-    if constexpr (NR == 1 && QUANT)
+    if constexpr (NR == 1 && MB == 1 && MODE == Mode::kPlain)
         if (g.K % (512 * 8) == 0) return launch_one<NR, MB, 4, MODE, QUANT>(g, mtiles, stream);
     if (g.K % 256 == 0) return launch_one<NR, MB, 2, MODE, QUANT>(g, mtiles, stream);
     return launch_one<NR, MB, 1, MODE, QUANT>(g, mtiles, stream);
