@@ -25,6 +25,12 @@
 // scale bytes of a row would cost a request to L2 like the 128 bytes of its
 // codes; they come for RSTEP steps at a time into a ring of their own.
 // Blocks past K and rows past the operand load as zeros.
+//
+// Bound by the matrix units' power on large plain products (4096 x 6144 x
+// 16384 on MI355X: 220 us, 3.75 PFLOP/s; the instruction alone keeps 3.8 to 4.0
+// on random codes), by the weights on the routed layer (4096 tokens, 8 of 256
+// experts of 6144 x 2048: 820 us for 3.8 GB and 480 us for 2.2 GB, read and
+// written).
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 #include "nvfp4_dma.hpp"

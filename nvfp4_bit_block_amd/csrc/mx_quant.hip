@@ -4,7 +4,8 @@
 // Rows are whole blocks, so the rowwise passes run over the flat tensor: a
 // lane takes 8 elements (16 bytes), a quad of lanes one block.  Bound by
 // memory: 2 bytes read and 17/32 written per element (the reverse for
-// dequantize).
+// dequantize); 65536 x 6144, 1.02 GB, takes 148 us each on MI355X, 6.9 TB/s with
+// what the cache keeps, against 5.0 TB/s of a large copy.
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 
