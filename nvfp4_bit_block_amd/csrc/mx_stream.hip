@@ -25,6 +25,7 @@
 //   kGroupUp, kGroupDown  the same products on expert-sorted rows (up to 16
 //              of one expert per workgroup).
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
@@ -165,6 +166,24 @@ struct SliceItem {
     }
 };
 
+// The same for packed rows, which are only copied: a lane then loads its piece
+// of the activation once, not with every unit of weights.
+struct PackedItem {
+    u32x4 c;
+    uint32_t s;
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t KB, int b0, int blocks, int i) {
+        const int m = i / blocks, b = b0 + i - m * blocks;
+        c = *reinterpret_cast<const u32x4*>(codes + m * KB + (int64_t)b * 16);
+        s = scales[m * (KB / 16) + b];
+    }
+    __device__ __forceinline__ void store(uint8_t* lc, uint8_t* ls, int cap, int blocks, int i) {
+        const int m = i / blocks, b = i - m * blocks;
+        asm("" : "+v"(s));
+        *reinterpret_cast<u32x4*>(lc + ((size_t)m * cap + b) * 16) = c;
+        ls[(size_t)m * cap + b] = (uint8_t)s;
+    }
+};
+
 // D units in flight: their weights, and the packed activations (A_LDS: these
 // are in LDS, and read when they are used).
 //
@@ -237,16 +256,20 @@ struct Stream {
 
 enum class Mode : int { kPlain = 0, kSlotUp = 1, kSlotDown = 2, kGroupUp = 3, kGroupDown = 4 };
 
-// QUANT: the activation is bf16 and each wave quantizes its K slice into
-// LDS (kPlain: up to 16 rows; kSlotUp).  The LDS of a wave: `slice` blocks
-// per row.
-template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT, int D>
+// SRC: each wave reads the activation, packed, from memory as it goes; or
+// first quantizes its K slice of a bf16 activation into LDS, or copies that of
+// a packed one.  The LDS of a wave: `slice` blocks per row.
+enum class Src : int { kMemory = 0, kQuantize = 1, kCopy = 2 };
+
+template <int NR, int MB, int USTEPS, Mode MODE, Src SRC, int D>
 __global__ __launch_bounds__(64 * waves_of(NR)) __attribute__((amdgpu_waves_per_eu(wpe_of(NR, MB))))
 void k_mx_stream(MxStreamArgs g) {
     constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
     constexpr bool kUp = MODE == Mode::kSlotUp || MODE == Mode::kGroupUp;
     static_assert(!kUp || NR == 4, "gate/up: two tiles each");
-    Stream<NR, MB, USTEPS, D, QUANT> st;
+    constexpr bool kLds = SRC != Src::kMemory;
+    static_assert(MB == 1 || !kLds, "LDS holds up to 16 rows");
+    Stream<NR, MB, USTEPS, D, kLds> st;
     extern __shared__ __align__(16) uint8_t smem[];
     float* const red = reinterpret_cast<float*>(smem);  // [wave][tile][lane][4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -299,6 +322,35 @@ void k_mx_stream(MxStreamArgs g) {
         for (int i = 0; i < NR; ++i) st.w_at[i] = {w_row(i) * (uint32_t)KB + 16u * lg, w_row(i) * (uint32_t)KS};
     };
 
+    // units [u0, u1) of `rows` activation rows into this wave's own LDS, the
+    // first loads of them before those of the weights and stored after; the
+    // operand reads see them through pointers that start at unit 0
+    auto stage = [&](int rows, int u0, int u1, const uint16_t* x, const uint8_t* codes, const uint8_t* scales) {
+        constexpr int kBpu = 4 * USTEPS;  // blocks per unit
+        const int b0 = u0 * kBpu, blocks = max(min(u1 * kBpu, nblk) - b0, 0);
+        const int cap = g.slice;  // blocks a wave's row may hold, a multiple of 16
+        uint8_t* const lc = smem + (size_t)wave * rows * cap * 17;
+        uint8_t* const ls = lc + (size_t)rows * cap * 16;
+        const int items = rows * blocks;
+        auto copy = [&](auto item, auto load) {
+            if (lane < items) load(item, lane);
+            st.start(u0, u1, lg, nblk);
+            if (lane < items) item.store(lc, ls, cap, blocks, lane);
+            for (int i = lane + 64; i < items; i += 64) {
+                load(item, i);
+                item.store(lc, ls, cap, blocks, i);
+            }
+        };
+        if constexpr (SRC == Src::kQuantize)
+            copy(SliceItem(), [&](SliceItem& it, int i) { it.load(x, g.K, b0, blocks, i); });
+        else
+            copy(PackedItem(), [&](PackedItem& it, int i) { it.load(codes, scales, KB, b0, blocks, i); });
+        const int mr = l16 < rows ? l16 : 0;
+        st.a_codes = lc + (mr * cap - b0) * 16;
+        st.a_scales = ls + mr * cap - b0;
+        __builtin_amdgcn_wave_barrier();
+    };
+
     f32x4 acc[NR][MB];
 #pragma unroll
     for (int i = 0; i < NR; ++i)
@@ -318,12 +370,15 @@ void k_mx_stream(MxStreamArgs g) {
             if (e < 0 || e >= g.E) continue;
             const float wj = g.slot_w[s];
             weights(e);
-            st.ar = {g.a_codes + s * KB, g.a_scales + s * KS, (uint32_t)KB, (uint32_t)KS};
-            st.a_at[0] = {16u * lg, 0u};
+            if constexpr (!kLds) {
+                st.ar = {g.a_codes + s * KB, g.a_scales + s * KS, (uint32_t)KB, (uint32_t)KS};
+                st.a_at[0] = {16u * lg, 0u};
+            }
             f32x4 part[NR][1];
 #pragma unroll
             for (int i = 0; i < NR; ++i) part[i][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            st.start(u0, u1, lg, nblk);
+            if constexpr (kLds) stage(1, u0, u1, nullptr, g.a_codes + s * KB, g.a_scales + s * KS);
+            else st.start(u0, u1, lg, nblk);
             st.run(part, u0, u1, lg, nblk);
 #pragma unroll
             for (int i = 0; i < NR; ++i)
@@ -333,29 +388,11 @@ void k_mx_stream(MxStreamArgs g) {
     } else {
         const int u0 = wave * units / kWaves, u1 = (wave + 1) * units / kWaves;
         weights(expert);
-        if constexpr (QUANT) {
-            // this wave's slice of every row, quantized into its own LDS; the
-            // operand reads below see it through pointers that start at unit 0
-            constexpr int kBpu = 4 * USTEPS;  // blocks per unit
-            const int b0 = u0 * kBpu, blocks = max(min(u1 * kBpu, nblk) - b0, 0);
-            const int rows = MODE == Mode::kPlain ? (int)g.M : 1;
-            const uint16_t* const x = g.x + (MODE == Mode::kPlain ? 0 : row_beg / g.top_k) * g.K;
-            const int cap = g.slice;  // blocks a wave's row may hold, a multiple of 16
-            uint8_t* const lc = smem + (size_t)wave * rows * cap * 17;
-            uint8_t* const ls = lc + (size_t)rows * cap * 16;
-            const int items = rows * blocks;
-            SliceItem first;
-            if (lane < items) first.load(x, g.K, b0, blocks, lane);
-            st.start(u0, u1, lg, nblk);
-            if (lane < items) first.store(lc, ls, cap, blocks, lane);
-            for (int i = lane + 64; i < items; i += 64) {
-                first.load(x, g.K, b0, blocks, i);
-                first.store(lc, ls, cap, blocks, i);
-            }
-            const int mr = l16 < rows ? l16 : 0;
-            st.a_codes = lc + (mr * cap - b0) * 16;
-            st.a_scales = ls + mr * cap - b0;
-            __builtin_amdgcn_wave_barrier();
+        if constexpr (SRC == Src::kQuantize)
+            stage(MODE == Mode::kPlain ? (int)g.M : 1, u0, u1, g.x + (MODE == Mode::kPlain ? 0 : row_beg / g.top_k) * g.K,
+                  nullptr, nullptr);
+        else if constexpr (SRC == Src::kCopy) {
+            stage((int)g.M, u0, u1, nullptr, g.a_codes, g.a_scales);
         } else {
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
@@ -368,8 +405,8 @@ void k_mx_stream(MxStreamArgs g) {
             st.start(u0, u1, lg, nblk);
         }
         st.run(acc, u0, u1, lg, nblk);
-        if constexpr (QUANT) __syncthreads();  // the sums below reuse the slices' LDS
     }
+    if constexpr (kLds) __syncthreads();  // the sums below reuse the slices' LDS
 
     // ---- the waves' sums, in wave order
 #pragma unroll
@@ -453,13 +490,13 @@ int rows_per_tile(int64_t N, int nr) {
 
 // Units in flight: 16 code loads a lane of weights alone, 8 and their
 // activation's (4 where the scale bytes come one by one); at least two units.
-template <int NR, int MB, int USTEPS, bool QUANT>
+template <int NR, int MB, int USTEPS, Src SRC>
 constexpr int units_in_flight() {
-    constexpr int steps = USTEPS == 1 ? 2 : QUANT ? 16 : MB == 1 ? 8 : 4;
+    constexpr int steps = USTEPS == 1 ? 2 : SRC != Src::kMemory ? 16 : MB == 1 ? 8 : 4;
     return std::max(2, steps / (USTEPS * NR));
 }
 
-template <int NR, int MB, int USTEPS, Mode MODE, bool QUANT>
+template <int NR, int MB, int USTEPS, Mode MODE, Src SRC>
 hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
     constexpr int kWaves = waves_of(NR), kThreads = 64 * kWaves;
     constexpr bool kUp = MODE == Mode::kSlotUp || MODE == Mode::kGroupUp;
@@ -468,31 +505,31 @@ hipError_t launch_one(MxStreamArgs g, int64_t mtiles, hipStream_t stream) {
     const int64_t wgs = mtiles * g.ntiles;
     if (wgs < 1 || wgs >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidValue;
     size_t lds = (size_t)kWaves * NR * MB * 1024;
-    if (QUANT) {
-        g.slice = slice_of(g.K, USTEPS, kWaves);
+    if (SRC != Src::kMemory) {
+        g.slice = slice_of(g.K, USTEPS, MODE == Mode::kSlotDown ? 1 : kWaves);  // (a wave may have a slot's whole row)
         lds = std::max(lds, (size_t)kWaves * (MODE == Mode::kPlain ? (size_t)g.M : 1) * g.slice * 17);
     }
     if (lds > 64 * 1024) return hipErrorInvalidValue;
     // (a unit past a wave's last still issues its loads: two where it has no
     // more; 37 x 4099 x 2080 with four 11.5, with two 9.6 us)
-    constexpr int D = units_in_flight<NR, MB, USTEPS, QUANT>();
+    constexpr int D = units_in_flight<NR, MB, USTEPS, SRC>();
     if constexpr (MODE == Mode::kPlain && D > 2)
         if (g.K <= (int64_t)2 * kWaves * 128 * USTEPS) {
-            hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, 2>), dim3((unsigned)wgs), dim3(kThreads), lds,
+            hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, SRC, 2>), dim3((unsigned)wgs), dim3(kThreads), lds,
                                stream, g);
             return hipGetLastError();
         }
-    hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, QUANT, D>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
+    hipLaunchKernelGGL((k_mx_stream<NR, MB, USTEPS, MODE, SRC, D>), dim3((unsigned)wgs), dim3(kThreads), lds, stream, g);
     return hipGetLastError();
 }
 
-template <int NR, int MB, Mode MODE, bool QUANT>
+template <int NR, int MB, Mode MODE, Src SRC>
 hipError_t launch_k(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
     // units of four steps where one tile's waves then share them evenly
     if constexpr (NR == 1 && MB == 1 && MODE == Mode::kPlain)
-        if (g.K % (512 * 8) == 0) return launch_one<NR, MB, 4, MODE, QUANT>(g, mtiles, stream);
-    if (g.K % 256 == 0) return launch_one<NR, MB, 2, MODE, QUANT>(g, mtiles, stream);
-    return launch_one<NR, MB, 1, MODE, QUANT>(g, mtiles, stream);
+        if (g.K % (512 * 8) == 0) return launch_one<NR, MB, 4, MODE, SRC>(g, mtiles, stream);
+    if (g.K % 256 == 0) return launch_one<NR, MB, 2, MODE, SRC>(g, mtiles, stream);
+    return launch_one<NR, MB, 1, MODE, SRC>(g, mtiles, stream);
 }
 
 }  // namespace
@@ -500,9 +537,10 @@ hipError_t launch_k(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
 // Every workgroup quantizes the rows for itself: 2 us for one row of 16384,
 // 7.5 us for four, against about 4 us for a launch of its own.  (LDS: the
 // largest of the forms, four waves, units of up to four steps.)
-bool mx_stream_quantizes(int64_t M, int64_t K) {
-    return M <= 2 && K <= ((int64_t)1 << 20) && (M * (K / 32 + 16 * 8) * 17) <= 64 * 1024;
+static bool fits_lds(int64_t M, int64_t K) {
+    return K <= ((int64_t)1 << 20) && M * (K / 32 + 16 * 8) * 17 <= 64 * 1024;
 }
+bool mx_stream_quantizes(int64_t M, int64_t K) { return M <= 2 && fits_lds(M, K); }
 bool mx_slots_fit(int64_t H) { return mx_stream_quantizes(1, H); }
 
 // 16-row weight tiles of a wave in the plain form: one while that gives at most
@@ -527,33 +565,36 @@ bool mx_stream_takes(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mx_stream(const MxStreamArgs& g, hipStream_t stream) {
     const int nr = plain_tiles(g.M, g.N, g.K);
-    if (g.x != nullptr)
-        return nr == 1 ? launch_k<1, 1, Mode::kPlain, true>(g, 1, stream)
-                       : nr == 2 ? launch_k<2, 1, Mode::kPlain, true>(g, 1, stream)
-                                 : launch_k<4, 1, Mode::kPlain, true>(g, 1, stream);
+    auto rows16 = [&](auto src) {
+        constexpr Src S = decltype(src)::value;
+        return nr == 1 ? launch_k<1, 1, Mode::kPlain, S>(g, 1, stream)
+                       : nr == 2 ? launch_k<2, 1, Mode::kPlain, S>(g, 1, stream)
+                                 : launch_k<4, 1, Mode::kPlain, S>(g, 1, stream);
+    };
+    if (g.x != nullptr) return rows16(std::integral_constant<Src, Src::kQuantize>{});
     if (g.M <= 16)
-        return nr == 1 ? launch_k<1, 1, Mode::kPlain, false>(g, 1, stream)
-                       : nr == 2 ? launch_k<2, 1, Mode::kPlain, false>(g, 1, stream)
-                                 : launch_k<4, 1, Mode::kPlain, false>(g, 1, stream);
+        return fits_lds(g.M, g.K) ? rows16(std::integral_constant<Src, Src::kCopy>{})
+                                  : rows16(std::integral_constant<Src, Src::kMemory>{});
     if (g.M <= 32)
-        return nr == 1 ? launch_k<1, 2, Mode::kPlain, false>(g, 1, stream)
-                       : launch_k<2, 2, Mode::kPlain, false>(g, 1, stream);
+        return nr == 1 ? launch_k<1, 2, Mode::kPlain, Src::kMemory>(g, 1, stream)
+                       : launch_k<2, 2, Mode::kPlain, Src::kMemory>(g, 1, stream);
     if (g.M <= 64)
-        return launch_k<1, 4, Mode::kPlain, false>(g, 1, stream);
+        return launch_k<1, 4, Mode::kPlain, Src::kMemory>(g, 1, stream);
     return hipErrorInvalidValue;
 }
 
 hipError_t launch_mx_slot_up(const MxStreamArgs& g, int64_t slots, hipStream_t stream) {
-    return launch_k<4, 1, Mode::kSlotUp, true>(g, slots, stream);
+    return launch_k<4, 1, Mode::kSlotUp, Src::kQuantize>(g, slots, stream);
 }
 hipError_t launch_mx_slot_down(const MxStreamArgs& g, int64_t tokens, hipStream_t stream) {
-    return launch_k<1, 1, Mode::kSlotDown, false>(g, tokens, stream);
+    return fits_lds(8, g.K) ? launch_k<1, 1, Mode::kSlotDown, Src::kCopy>(g, tokens, stream)
+                            : launch_k<1, 1, Mode::kSlotDown, Src::kMemory>(g, tokens, stream);
 }
 hipError_t launch_mx_group_up(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
-    return launch_k<4, 1, Mode::kGroupUp, false>(g, mtiles, stream);
+    return launch_k<4, 1, Mode::kGroupUp, Src::kMemory>(g, mtiles, stream);
 }
 hipError_t launch_mx_group_down(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
-    return launch_k<4, 1, Mode::kGroupDown, false>(g, mtiles, stream);
+    return launch_k<4, 1, Mode::kGroupDown, Src::kMemory>(g, mtiles, stream);
 }
 
 }  // namespace nvfp4
