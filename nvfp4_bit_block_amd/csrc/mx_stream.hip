@@ -3,8 +3,8 @@
 // registers, and nothing else is large.  Bound by the weight stream, and by a
 // launch's ramp and tail where that is short: on MI355X one token through 6144
 // x 16384 takes 10.9 us (53.5 MB, 4.9 TB/s), the gate/up product of its 8
-// experts of 6144 x 2048 23.8 us (107 MB, 4.5 TB/s) and the down product 14.5
-// us (53.5 MB, 3.7 TB/s).
+// experts of 6144 x 2048 23.8 us (107 MB, 4.5 TB/s) and the down product 11.9
+// us (53.5 MB, 4.5 TB/s).
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4, weights as the A operand (16 weight
 // rows), activations as the B operand (16 rows, fewer are padded with copies
@@ -167,7 +167,9 @@ struct SliceItem {
 };
 
 // The same for packed rows, which are only copied: a lane then loads its piece
-// of the activation once, not with every unit of weights.
+// of the activation once, where the operand's layout has every 16 lanes load a
+// row again with each unit of weights (one packed row through 6144 x 16384 16.0
+// -> 12.9 us, the down product of a token's 8 experts 14.8 -> 11.9).
 struct PackedItem {
     u32x4 c;
     uint32_t s;
@@ -553,7 +555,7 @@ static int plain_tiles(int64_t M, int64_t N, int64_t K) {
 }
 
 // Every workgroup reads the activation, so with more rows that becomes the
-// larger stream: at 6144 x 16384 4 rows take 16.7 us, 8 18.6, 16 22 and 64 57,
+// larger stream: at 6144 x 16384 4 rows take 14.5 us, 8 18.6, 16 22 and 64 57,
 // where the LDS tiles take 17 for up to 16 and 21 for 64; 32 rows of 16384 x
 // 2048 take 10 us either way.
 bool mx_stream_takes(int64_t M, int64_t N, int64_t K) {

@@ -409,3 +409,16 @@ def test_experts_slot_by_slot(T, E, k, H, I):
     rng = np.random.default_rng(T * E + k)
     case = _experts_case(rng, T, E, k, H, I, skip=0.1)
     _check_experts(_run_experts(*case), *case)
+
+
+# activations too large for the waves' LDS
+@pytest.mark.parametrize("M,N,K", [(12, 70, 8192), (12, 70, 8448), (16, 8200, 4352), (16, 33, 8224)])
+def test_product_streaming_from_memory(M, N, K):
+    test_product(M, N, K)
+
+
+@pytest.mark.parametrize("T,I", [(1, 11520), (2, 11552)])
+def test_experts_wide_slots(T, I):
+    rng = np.random.default_rng(I)
+    case = _experts_case(rng, T, 4, 2, 64, I)
+    _check_experts(_run_experts(*case), *case)
