@@ -72,8 +72,6 @@ int32_t nvfp4_mx_gemm_packed(const uint8_t* a_codes, const uint8_t* a_scales, in
  *   h = bf16(silu(g) * u);  h^ = MXFP4(h)
  *   out[t] = bf16( sum_j topk_weights[t, j] * (h^ * W2_e^T) )
  * products and sums in fp32, slots in order; a token without a slot gets 0.
- * With many slots (the layer then sorts them by expert) each slot's product
- * h^ * W2_e^T is rounded to bf16 before the sum.
  * x bf16 [T, H]; topk_ids int32 [T, top_k]; topk_weights fp32 [T, top_k];
  * w13_codes [E, 2I, H/2], w13_scales [E, 2I, H/32]; w2_codes [E, H, I/2],
  * w2_scales [E, H, I/32]; out bf16 [T, H].

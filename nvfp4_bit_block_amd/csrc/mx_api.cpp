@@ -151,7 +151,7 @@ MxMoeLayout layout_mx_moe(const nvfp4_mx_moe_problem& p) {
     l.xs = off; off += packed_scales_bytes(p.T, p.H);
     l.hc = off; off += packed_codes_bytes(S, p.I);
     l.hs = off; off += packed_scales_bytes(S, p.I);
-    l.y = off; off += align_up((size_t)S * (size_t)p.H * 2);
+    l.y = off; off += align_up((size_t)S * (size_t)p.H * 4);
     l.total = off;
     return l;
 }
@@ -370,7 +370,7 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
     uint8_t* xs = at<uint8_t>(workspace, l.xs);
     uint8_t* hc = at<uint8_t>(workspace, l.hc);
     uint8_t* hs = at<uint8_t>(workspace, l.hs);
-    uint16_t* Y = at<uint16_t>(workspace, l.y);
+    float* Y = at<float>(workspace, l.y);
     int32_t st;
     if (S <= kMxPrepareSlots) {
         const MxPrepareArgs a = {t->topk_ids, (int32_t)S, E, bm, row_off, tile_off, perm, inv, t->x, p->T * (p->H / 8),
@@ -392,7 +392,7 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
         up.perm = perm;
         up.row_off = down.row_off = row_off;
         up.tile_off = down.tile_off = tile_off;
-        down.y = Y;
+        down.slot_y = Y;
         st = api_hip(launch_mx_group_up(up, grid_m, s), "mx_moe gate/up");
         if (st) return st;
         st = api_hip(launch_mx_group_down(down, grid_m, s), "mx_moe down");
@@ -433,7 +433,7 @@ int32_t nvfp4_mx_moe(const nvfp4_mx_moe_problem* p, const nvfp4_mx_moe_tensors* 
     g2.groups = E;
     g2.out = Y;
     g2.ldo = p->H;
-    st = api_hip(launch_mx_gemm(g2, MxEpi::kStoreBf16, grid_m, s), "mx_moe down");
+    st = api_hip(launch_mx_gemm(g2, MxEpi::kStoreF32, grid_m, s), "mx_moe down");
     if (st) return st;
     return api_hip(launch_mx_combine(Y, inv, t->topk_weights, p->T, (int32_t)p->top_k, p->H, t->out, s),
                    "mx_moe combine");

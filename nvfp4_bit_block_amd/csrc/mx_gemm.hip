@@ -29,7 +29,7 @@
 // Bound by the matrix units' power on large plain products (4096 x 6144 x
 // 16384 on MI355X: 220 us, 3.75 PFLOP/s; the instruction alone keeps 3.8 to 4.0
 // on random codes), by the weights on the routed layer (4096 tokens, 8 of 256
-// experts of 6144 x 2048: 820 us for 3.8 GB and 480 us for 2.2 GB, read and
+// experts of 6144 x 2048: 807 us for 3.8 GB and 530 us for 2.6 GB, read and
 // written).
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
     __builtin_amdgcn_s_waitcnt(kWaitAll);
 
     // (the slabs below reuse the stages, which other waves may still read)
-    if constexpr (EP == MxEpi::kStoreBf16) __syncthreads();
+    if constexpr (EP == MxEpi::kStoreBf16 || EP == MxEpi::kStoreF32) __syncthreads();
 
     // ---- epilogue: acc[j][i][r] is weight row 32 j + 8 (r / 4) + 4 hf + r % 4
     // of the wave, activation row 32 (i WM + wm) + c32.
@@ -443,25 +443,37 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(MxGemmArgs g) {
             // a 32-row slab of the wave's tile meets in LDS and leaves as
             // 16-byte pieces of rows (pitch: 16 rows' 8-byte writes fall on
             // different banks)
-            constexpr int kPitch = WTN * 2 + 16;
+            constexpr bool kF32 = EP == MxEpi::kStoreF32;
+            constexpr int kPitch = WTN * (kF32 ? 4 : 2) + 16;
             static_assert(NW * 32 * kPitch <= SC_OFF, "epilogue slabs");
             uint8_t* const slab = smem + wave * 32 * kPitch;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    *reinterpret_cast<uint2*>(slab + c32 * kPitch + 2 * (32 * j + 8 * p + 4 * hf)) =
-                        make_uint2(pack_bf16(acc[j][i][4 * p], acc[j][i][4 * p + 1]),
-                                   pack_bf16(acc[j][i][4 * p + 2], acc[j][i][4 * p + 3]));
+                for (int p = 0; p < 4; ++p) {
+                    const int at = 32 * j + 8 * p + 4 * hf;
+                    const float v0 = acc[j][i][4 * p], v1 = acc[j][i][4 * p + 1];
+                    const float v2 = acc[j][i][4 * p + 2], v3 = acc[j][i][4 * p + 3];
+                    if constexpr (kF32)
+                        *reinterpret_cast<f32x4*>(slab + c32 * kPitch + 4 * at) = f32x4{v0, v1, v2, v3};
+                    else
+                        *reinterpret_cast<uint2*>(slab + c32 * kPitch + 2 * at) =
+                            make_uint2(pack_bf16(v0, v1), pack_bf16(v2, v3));
+                }
             __builtin_amdgcn_wave_barrier();
             const int64_t row0 = row_beg + 32 * (i * WM + wm);
             const bool vec = (g.ldo & 7) == 0;
+            constexpr int kPieces = WTN * (kF32 ? 4 : 2) / 16;  // of a row
 #pragma unroll
-            for (int p = 0; p < 2 * TN; ++p) {
-                const int e = 64 * p + lane, rr = e / (4 * TN), ch = e % (4 * TN);
+            for (int p = 0; p < kPieces / 2; ++p) {
+                const int e = 64 * p + lane, rr = e / kPieces, ch = e % kPieces;
                 const uint4 v = *reinterpret_cast<const uint4*>(slab + rr * kPitch + 16 * ch);
-                const int64_t col = n0 + wn * WTN + 8 * ch;
+                const int64_t col = n0 + wn * WTN + (kF32 ? 4 : 8) * ch;
                 if (row0 + rr >= row_end || col >= nlim) continue;
+                if constexpr (kF32) {  // (ldo is a multiple of 32)
+                    *reinterpret_cast<uint4*>(reinterpret_cast<float*>(g.out) + (row0 + rr) * g.ldo + col) = v;
+                    continue;
+                }
                 uint16_t* const dst = reinterpret_cast<uint16_t*>(g.out) + (row0 + rr) * g.ldo + col;
                 if (vec && col + 8 <= nlim) {
                     *reinterpret_cast<uint4*>(dst) = v;
@@ -553,11 +565,11 @@ hipError_t launch_mx_gemm_split(const MxGemmArgs& g0, float* partial, hipStream_
 // main loop counts an expert's rows by 32.  Gate/up and down of 256 experts of
 // 6144 x 2048, top 8 (us; 2 x 2 waves, which count them by 64, in brackets):
 // 4096 tokens 831 and 486 (846, 486), 2560 738 and 415 (752, 426), 640 648 and
-// 368 (659, 375).
+// 368 (659, 375), the down product with bf16 stores; fp32 ones make the 486 530.
 hipError_t launch_mx_gemm(const MxGemmArgs& g, MxEpi epi, int grid_m, hipStream_t stream) {
     if (g.groups > 0)
         return epi == MxEpi::kGateUp ? launch_cfg<6, 2, 1, 4, 3, 2, MxEpi::kGateUp>(g, grid_m, stream)
-                                     : launch_cfg<6, 2, 1, 4, 3, 2, MxEpi::kStoreBf16>(g, grid_m, stream);
+                                     : launch_cfg<6, 2, 1, 4, 3, 2, MxEpi::kStoreF32>(g, grid_m, stream);
     // share of the CUs' time that a tile's rounds fill
     auto fill = [&](int64_t bm, int64_t bn, int64_t slots) {
         const int64_t t = ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn);

@@ -25,6 +25,7 @@ enum class MxEpi : int {
     kStoreBf16 = 0,  // y = bf16(acc)
     kGateUp = 1,     // h = bf16(silu(g) * u), stored as MXFP4
     kPartialF32 = 2, // partial[split] = acc (K split, joined afterwards)
+    kStoreF32 = 3,   // y = acc (grouped: slot outputs, summed afterwards)
 };
 
 struct MxGemmArgs {
@@ -43,7 +44,7 @@ struct MxGemmArgs {
     int32_t groups = 0;
     int32_t ntiles = 0;                 // set by the launcher
     int32_t ksplit = 1, ksteps = 0;     // kPartialF32: K splits and the steps of each
-    void* out = nullptr;                // kStoreBf16: bf16 [M, ldo]; kGateUp: codes [M, ldo/2]
+    void* out = nullptr;                // kStoreBf16, kStoreF32: bf16, fp32 [M, ldo]; kGateUp: codes [M, ldo/2]
     uint8_t* out_scales = nullptr;      // kGateUp: [M, ldo/32]
     int64_t ldo = 0;
 };
@@ -72,6 +73,7 @@ struct MxStreamArgs {
     const int32_t* row_off = nullptr;   // row and tile offsets as in MxGemmArgs
     const int32_t* tile_off = nullptr;
     uint16_t* y = nullptr;              // bf16 outputs
+    float* slot_y = nullptr;            // kGroupDown: fp32 outputs [S, N]
     uint8_t* h_codes = nullptr;         // gate/up forms: MXFP4 h [S, N/4], [S, N/64]
     uint8_t* h_scales = nullptr;
     int32_t ntiles = 0, slice = 0, rt = 16;  // set by the launcher
@@ -110,9 +112,9 @@ struct MxPrepareArgs {
 constexpr int64_t kMxPrepareSlots = 1 << 13;
 hipError_t launch_mx_prepare(const MxPrepareArgs& a, hipStream_t stream);
 
-// out[t] = bf16(sum_j w[t, j] * Y[inv[t * top_k + j]]) over expert-sorted bf16
+// out[t] = bf16(sum_j w[t, j] * Y[inv[t * top_k + j]]) over expert-sorted fp32
 // rows Y [S, H], slots in order, inv < 0 skipped; H % 32 == 0.
-hipError_t launch_mx_combine(const uint16_t* Y, const int32_t* inv, const float* w, int64_t T, int32_t top_k, int64_t H,
+hipError_t launch_mx_combine(const float* Y, const int32_t* inv, const float* w, int64_t T, int32_t top_k, int64_t H,
                              uint16_t* out, hipStream_t stream);
 
 // -------------------------------------------------------------------- gate --

@@ -23,7 +23,7 @@
 //              token's slots in order and weigh them, so the weighted sum
 //              leaves as bf16 without a pass of its own.
 //   kGroupUp, kGroupDown  the same products on expert-sorted rows (up to 16
-//              of one expert per workgroup).
+//              of one expert per workgroup); kGroupDown's leave as fp32.
 #include <algorithm>
 #include <type_traits>
 
@@ -453,7 +453,9 @@ void k_mx_stream(MxStreamArgs g) {
             const int64_t col = n0 + rt * (t / MB) + 4 * (ln >> 4);
             if (row >= row_end || col >= g.N || 4 * (ln >> 4) >= rt) continue;
             const f32x4 v = total(t, ln);
-            {
+            if constexpr (MODE == Mode::kGroupDown) {
+                *reinterpret_cast<f32x4*>(g.slot_y + row * g.N + col) = v;  // (N is a multiple of 32)
+            } else {
                 uint16_t* const dst = g.y + row * g.N + col;
                 const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
                 if ((g.N & 3) == 0) {
