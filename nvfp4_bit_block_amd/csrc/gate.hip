@@ -406,7 +406,9 @@ hipError_t gate_launch(const GateArgs& a, bool wide_key, bool backward, hipStrea
 
 template <int LPT, int NPL>
 hipError_t gate_types(const nvfp4_gate_config& c, const GateArgs& a, bool backward, hipStream_t s) {
-    const bool wide = a.bias != nullptr || (c.group_top == 2 && c.topk_group < c.n_group);
+    // (group_top = 2 orders by the score even where every group is kept: scores
+    // that are equal in 64 bits go by index, whatever their logits)
+    const bool wide = a.bias != nullptr || c.group_top == 2;
     const int which = (c.logits_dtype == NVFP4_GATE_BF16 ? 4 : 0) + (c.score == NVFP4_GATE_SIGMOID ? 2 : 0) +
                       (c.renormalize ? 1 : 0);
     switch (which) {
