@@ -170,8 +170,8 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 }
 
 bool mx_quantize_cols_fits(int64_t rows, int64_t cols) {
-    const int64_t rt = (rows + 255) / 256, ct = (cols + 63) / 64;
-    return rt < kMaxGrid && ct < kMaxGrid && rt * ct < kMaxGrid;
+    if (rows > 256 * kMaxGrid || cols > 64 * kMaxGrid) return false;  // (the sums and the product below stay in range)
+    return (rows + 255) / 256 * ((cols + 63) / 64) < kMaxGrid;
 }
 
 // 256-row tiles write whole cache lines of codes; below two of them per CU,
