@@ -48,7 +48,7 @@ int32_t check_gate(const nvfp4_gate_config* c, bool backward) {
 int32_t check_product(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K <= 0 || K % 32 != 0)
         return api_fail(NVFP4_ERR_SHAPE, "mx_gemm: need M, N >= 0, K > 0 and K % 32 == 0");
-    // (few rows: a workgroup of 256 threads for 32 or more columns)
+    // (few rows: a workgroup of 256 threads for 32 or more columns, where N is large)
     if (K >= ((int64_t)1 << 24) || M >= ((int64_t)1 << 30) || N >= ((int64_t)1 << 28) ||
         (N > 0 && M > (((int64_t)1 << 36) / N)))
         return api_fail(NVFP4_ERR_UNSUPPORTED, "mx_gemm: K below 2^24, M below 2^30, N below 2^28, M * N up to 2^36");

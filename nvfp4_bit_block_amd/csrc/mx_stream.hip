@@ -548,11 +548,12 @@ bool mx_stream_quantizes(int64_t M, int64_t K) { return M <= 2 && fits_lds(M, K)
 bool mx_slots_fit(int64_t H) { return mx_stream_quantizes(1, H); }
 
 // 16-row weight tiles of a wave in the plain form: one while that gives at most
-// 512 workgroups or the rows are long, else two or (up to 16 activation rows)
-// four.
+// 512 workgroups or the rows are long (and a launch holds them: fewer than 2^23
+// workgroups of 512 threads, two to a tile at most), else two or (up to 16
+// activation rows) four.
 static int plain_tiles(int64_t M, int64_t N, int64_t K) {
     const int64_t t1 = (N + 15) / 16;
-    const int nr = t1 <= 512 || K >= 8192 ? 1 : t1 <= 1024 ? 2 : 4;
+    const int nr = t1 <= 512 || (K >= 8192 && t1 < (1 << 22)) ? 1 : t1 <= 1024 ? 2 : 4;
     return M <= 16 ? nr : M <= 32 ? std::min(nr, 2) : 1;
 }
 
