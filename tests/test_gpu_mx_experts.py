@@ -21,6 +21,33 @@ CASES = [
     (2, 60, 8, 4, 544, 352, 0.1, 0, ROWS192),
     (3, 40, 32, 4, 256, 96, 0.0, 40, ROWS16),
     (4, 3, 16, 4, 512, 96, 0.0, 0, SLOTS),
+    # slots: K units of two steps and of one in either product, one token and
+    # several, the most slots
+    (5, 1, 8, 2, 256, 256, 0.0, 0, SLOTS),
+    (6, 1, 8, 8, 512, 512, 0.0, 0, SLOTS),
+    (7, 2, 16, 3, 96, 768, 0.2, 0, SLOTS),
+    (8, 7, 40, 9, 96, 64, 0.0, 0, SLOTS),
+    (9, 1, 200, 128, 64, 32, 0.1, 0, SLOTS),
+    (10, 16, 256, 8, 64, 32, 0.0, 0, SLOTS),
+    # rows of h too long for the waves' LDS
+    (11, 1, 4, 2, 64, 11520, 0.0, 0, SLOTS),
+    (12, 2, 4, 2, 64, 11552, 0.0, 0, SLOTS),
+    # one slot more than the slot form takes; several row tiles of an expert,
+    # whole and with one row
+    (13, 43, 200, 3, 64, 32, 0.0, 43, ROWS16),
+    (14, 40, 32, 4, 256, 256, 0.1, 33, ROWS16),
+    (15, 64, 32, 5, 512, 512, 0.0, 48, ROWS16),
+    (16, 48, 40, 4, 96, 544, 0.0, 17, ROWS16),
+    (17, 33, 24, 5, 1024, 128, 0.2, 20, ROWS16),
+    # tiles of whole and odd blocks, one expert, a row past a tile
+    (18, 61, 4, 3, 544, 352, 0.0, 0, ROWS192),
+    (19, 400, 2, 2, 256, 512, 0.0, 0, ROWS192),
+    (20, 193, 1, 1, 128, 128, 0.0, 0, ROWS192),
+    (21, 300, 5, 3, 160, 96, 0.1, 100, ROWS192),
+    # many experts, and many slots (sorted by several launches)
+    (22, 40, 4096, 8, 64, 32, 0.0, 40, ROWS16),
+    (23, 1100, 600, 8, 64, 32, 0.1, 0, ROWS16),
+    (24, 2100, 20, 4, 160, 96, 0.1, 0, ROWS192),
 ]
 
 
@@ -56,3 +83,29 @@ def test_every_row(case):
     y, plan = run_and_plan(*args)
     assert plan == case[-1]
     mx_bounds.check(y, *mx_bounds.experts(*args))
+
+
+@pytest.mark.parametrize("T,plan", [(1, SLOTS), (200, ROWS16), (2500, ROWS192)])
+def test_last_expert_past_32_bits(T, plan):
+    """600 experts, the last one's weights past 2 GiB, in each plan; the other
+    experts' weights decode as NaN."""
+    E, H, I = 600, 2048, 2048
+    x, _, tw, w13, w2 = mx_bounds.experts_case(T, T, 1, 1, H, I)
+    d = device()
+    assert (E - 1) * w13[0].size > 2 ** 31
+    full = []
+    for t in (*w13, *w2):
+        big = torch.full((E, *t.shape[1:]), 255, dtype=torch.uint8, device=d)
+        big[-1] = torch.from_numpy(t[0])
+        full.append(big)
+    ids = torch.full((T, 1), E - 1, dtype=torch.int32, device=d)
+    ws = torch.zeros(nv.mx_moe_workspace_size(T, E, 1, H, I), dtype=torch.uint8, device=d)
+    y = nv.mx_moe(dev_bf16(x), ids, dev(tw), *full, ws=ws)
+    if plan != SLOTS:
+        tiles = ws[_align(4 * (E + 1)):][:4 * (E + 1)].cpu().numpy().view(np.int32)
+        assert tiles[-1] == -(-T // (16 if plan == ROWS16 else 192))
+    else:
+        assert ws.numel() == _align(T * I // 2) + _align(T * I // 32)
+    some = np.linspace(0, T - 1, min(T, 200)).astype(int)           # of the rows, the first and the last
+    args = (x[some], np.zeros((some.size, 1), np.int32), tw[some], w13, w2)
+    mx_bounds.check(host_bf16_f32(y).astype(np.float64)[some], *mx_bounds.experts(*args))
