@@ -47,13 +47,13 @@ def experts_case(seed, T, E, k, H, I, skip=0.0, skew=0):
     return x, ids, tw, w13, w2
 
 
-def _quantum(codes, scales):
+def quantum(codes, scales):
     """Per row: half the least scale of a block that holds anything."""
     some = (codes.reshape(*scales.shape, 16) & 0x77).any(axis=-1)
     return np.exp2(np.where(some, scales, 254).astype(np.float64).min(axis=-1) - 128.0)
 
 
-def _sum_error(a, aq, w, wq):
+def sum_error(a, aq, w, wq):
     """|a| |w|^T and what an fp32 sum of a w^T may be off by, in any order."""
     mag = np.abs(a) @ np.abs(w).T
     exact = mag < 2.0 ** 20 * aq[:, None] * wq[None, :]
@@ -90,7 +90,7 @@ def requantize(h, rel):
     for v in (lo, hi):
         for s in (s_lo, s_hi):
             flip = np.maximum(flip, np.abs(_encode_as(v, s) - n))
-    return nominal, _quantum(*packed), flip.reshape(R, I)
+    return nominal, quantum(*packed), flip.reshape(R, I)
 
 
 def experts(x, ids, tw, w13, w2):
@@ -99,21 +99,21 @@ def experts(x, ids, tw, w13, w2):
     T, H = x.shape
     I = w2[0].shape[-1] * 2
     xp = ref.mx_encode(x)
-    xh, xq = ref.mx_decode(*xp), _quantum(*xp)
+    xh, xq = ref.mx_decode(*xp), quantum(*xp)
     out, slack, mags = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
     for e in range(w13[0].shape[0]):
         t, j = np.nonzero(ids == e)
         if not t.size:
             continue
         w = ref.mx_decode(w13[0][e], w13[1][e])
-        _, off = _sum_error(xh[t], xq[t], w, _quantum(w13[0][e], w13[1][e]))
+        _, off = sum_error(xh[t], xq[t], w, quantum(w13[0][e], w13[1][e]))
         assert (off == 0).all(), "gate/up sums are not exact"
         gu = xh[t] @ w.T
         g, u = gu[:, :I], gu[:, I:]
         assert np.abs(g).max() < 80.0
         hh, hq, flip = requantize(g / (1.0 + np.exp(-g)) * u, (2 * np.abs(g) + 8) * 2.0 ** -24)
         w = ref.mx_decode(w2[0][e], w2[1][e])
-        mag, off = _sum_error(hh, hq, w, _quantum(w2[0][e], w2[1][e]))
+        mag, off = sum_error(hh, hq, w, quantum(w2[0][e], w2[1][e]))
         c = tw[t, j, None].astype(np.float64)
         np.add.at(out, t, (hh @ w.T) * c)
         np.add.at(mags, t, mag * c)

@@ -1,0 +1,59 @@
+"""MXFP4 products on the large tiles (256 x 192 and 256 x 256, which take about
+a tile for every CU), bit for bit.
+
+The scale bytes lie so close together that every sum is a whole number of
+quanta below 2^20 of them, in any order: fp32 holds them all, and the one
+rounding to bf16 is the definition's."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_bit_block_amd as nv
+import workloads as wl
+from tests import mx_bounds
+from tests import mx_reference as ref
+from tests.gpu_common import dev, dev_bf16, device, host_bf16_f32
+
+pytestmark = pytest.mark.gpu
+
+# 2048 x 6144: 256 tiles of 256 x 192, against 192 of 256 x 256 and one and a
+# half rounds of 128 x 128; K from less than one step of 256 to many, whole and
+# odd numbers of 128 and (through the unaligned form) of 32
+TILES_192 = [(2048, 6144, 128), (2048, 6144, 384), (2000, 6141, 256), (1793, 6139, 640), (2048, 6144, 2048), (2037, 6100, 8320),
+             (2048, 6144, 32), (2000, 6141, 96), (2048, 6144, 160), (1800, 6139, 544), (2048, 6144, 1056), (2037, 6100, 8224)]
+# 4096 x 4096: 256 tiles of 256 x 256
+TILES_256 = [(4096, 4096, 128), (4096, 4096, 256), (4001, 4093, 384), (3841, 4089, 512), (4096, 4096, 896), (4090, 4095, 2176)]
+
+
+def _exact(a, w):
+    off = mx_bounds.sum_error(ref.mx_decode(*a), mx_bounds.quantum(*a), ref.mx_decode(*w), mx_bounds.quantum(*w))[1]
+    assert (off == 0).all(), "sums are not exact"
+    return ref.bf16_values(ref.bf16_round(ref.product(a, w)))
+
+
+@pytest.mark.parametrize("M,N,K", TILES_192 + TILES_256)
+def test_large_tiles(M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    a, w = ref.random_mx(rng, M, K, lo=126, hi=128), ref.random_mx(rng, N, K, lo=121, hi=123)
+    ws = torch.full((max(16, nv.mx_gemm_packed_workspace_size(M, N, K)),), 255, dtype=torch.uint8, device=device())
+    out = torch.full((M + 1, N), 3.0, dtype=torch.bfloat16, device=device())
+    ad, wd = (dev(a[0]), dev(a[1])), (dev(w[0]), dev(w[1]))
+    nv.mx_gemm_packed(*ad, *wd, out=out[:M], ws=ws)
+    assert np.array_equal(host_bf16_f32(out[:M]).astype(np.float64), _exact(a, w))
+    assert (out[M] == 3.0).all()
+    assert torch.equal(nv.mx_gemm_packed(*ad, *wd), out[:M])       # and again
+
+
+def test_weight_gradient_of_a_training_batch():
+    """dW = dY^T X of 544 tokens from columnwise copies, on the unaligned 256 x
+    192 tiles."""
+    rng = np.random.default_rng(7)
+    T, N, K = 544, 2048, 6144
+    dy, x = wl.normal_bf16(rng, (T, N), 1.0), wl.normal_bf16(rng, (T, K), 1.0)
+    got = nv.mx_gemm_packed(*nv.mx_quantize_columnwise(dev_bf16(dy)), *nv.mx_quantize_columnwise(dev_bf16(x)))
+    a, w = (ref.mx_encode(np.ascontiguousarray(v.T)) for v in (dy, x))
+    want = ref.product(a, w)
+    off = mx_bounds.sum_error(ref.mx_decode(*a), mx_bounds.quantum(*a), ref.mx_decode(*w), mx_bounds.quantum(*w))[1]
+    assert (off == 0).mean() > 0.99                                 # (where a row holds a small block: 2^-23 K)
+    err = np.abs(host_bf16_f32(got).astype(np.float64) - want)
+    assert (err <= off + 2.0 ** -8 * (np.abs(want) + off)).all()
