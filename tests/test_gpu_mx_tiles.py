@@ -1,5 +1,5 @@
-"""MXFP4 products on the large tiles (256 x 192 and 256 x 256, which take about
-a tile for every CU), bit for bit.
+"""MXFP4 products bit for bit: on the large tiles (256 x 192 and 256 x 256,
+which take about a tile for every CU), and in every smaller form.
 
 The scale bytes lie so close together that every sum is a whole number of
 quanta below 2^20 of them, in any order: fp32 holds them all, and the one
@@ -57,3 +57,31 @@ def test_weight_gradient_of_a_training_batch():
     assert (off == 0).mean() > 0.99                                 # (where a row holds a small block: 2^-23 K)
     err = np.abs(host_bf16_f32(got).astype(np.float64) - want)
     assert (err <= off + 2.0 ** -8 * (np.abs(want) + off)).all()
+
+
+# the streaming kernel's forms, the 128 x 128 tiles and their K splits, as in
+# tests/test_gpu_mx.py
+SMALL = [(1, 16, 32), (1, 1, 64), (1, 257, 4096), (2, 40, 96), (5, 4099, 512), (8, 100, 2080), (16, 64, 1024), (17, 33, 544),
+         (33, 130, 256), (64, 256, 768), (100, 70, 1312), (128, 128, 512), (129, 257, 288), (300, 515, 2048),
+         (257, 256, 8192), (65, 129, 4096), (70, 33, 4128), (200, 255, 8224), (128, 6, 16384), (520, 700, 2304),
+         (2, 6144, 4096), (1, 70, 16384), (1, 70, 8448), (1, 70, 8480), (3, 70, 8448), (4, 33, 8224), (1, 8200, 4352),
+         (2, 8209, 160), (1, 16500, 544), (20, 100, 2304), (20, 8200, 256), (40, 130, 1280), (64, 65, 2080),
+         (12, 70, 8192), (12, 70, 8448), (16, 8200, 4352), (16, 33, 8224)]
+
+
+@pytest.mark.parametrize("M,N,K", SMALL)
+def test_smaller_forms(M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    a, w = ref.random_mx(rng, M, K, lo=126, hi=128), ref.random_mx(rng, N, K, lo=121, hi=123)
+    wd = (dev(w[0]), dev(w[1]))
+    want = _exact(a, w)
+    got = nv.mx_gemm_packed(dev(a[0]), dev(a[1]), *wd)
+    assert np.array_equal(host_bf16_f32(got).astype(np.float64), want)
+    # a bf16 activation whose MXFP4 is `a`: a block's scale stays where it is if
+    # its largest code is 4 or 6
+    v = ref.mx_decode(*a).reshape(M, K // 32, 32)
+    v[..., 0] = 6 * np.exp2(a[1] - 127.0)
+    v = v.reshape(M, K)
+    x = ref.bf16_round(v)
+    got = nv.mx_gemm(dev_bf16(x), *wd)
+    assert np.array_equal(host_bf16_f32(got).astype(np.float64), _exact(ref.mx_encode(x), w))
