@@ -371,15 +371,14 @@ __global__ __launch_bounds__(gate_threads(LPT)) void k_gate_backward(GateArgs a)
             const float4 v = *reinterpret_cast<const float4*>(row + e);
             if constexpr (BF16)
                 *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.dlogits) + base + e) =
-                    make_uint2(f32_to_bf16_rne(v.x) | (f32_to_bf16_rne(v.y) << 16),
-                               f32_to_bf16_rne(v.z) | (f32_to_bf16_rne(v.w) << 16));
+                    make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
             else
                 *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.dlogits) + base + e) = v;
         }
     } else {
         for (int e = q; e < a.E; e += LPT) {
             if constexpr (BF16)
-                reinterpret_cast<uint16_t*>(a.dlogits)[base + e] = (uint16_t)f32_to_bf16_rne(row[e]);
+                reinterpret_cast<uint16_t*>(a.dlogits)[base + e] = (uint16_t)pack_bf16(row[e], 0.0f);
             else
                 reinterpret_cast<float*>(a.dlogits)[base + e] = row[e];
         }

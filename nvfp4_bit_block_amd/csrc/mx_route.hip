@@ -132,7 +132,8 @@ __global__ __launch_bounds__(kPrepThreads) void k_mx_prepare(MxPrepareArgs a) {
 }
 
 // A thread sums 4 columns of one token; the rows of 8 slots are in flight
-// together (a skipped slot reads row 0 and is not added).
+// together (a skipped slot reads row 0 and is not added).  The NVFP4 layer's
+// sum rounds finite values only; this one keeps a NaN of any pattern.
 __global__ __launch_bounds__(256) void k_mx_combine(const float* __restrict__ Y, const int32_t* __restrict__ inv,
                                                     const float* __restrict__ w, int64_t total, int32_t top_k,
                                                     int32_t h4, uint16_t* __restrict__ out) {
