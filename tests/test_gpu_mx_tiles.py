@@ -85,3 +85,32 @@ def test_smaller_forms(M, N, K):
     x = ref.bf16_round(v)
     got = nv.mx_gemm(dev_bf16(x), *wd)
     assert np.array_equal(host_bf16_f32(got).astype(np.float64), _exact(ref.mx_encode(x), w))
+
+
+@pytest.mark.parametrize("M,K", [(8, 32), (8, 256), (80, 32), (80, 128), (80, 2080), (300, 8192)])
+def test_scale_bytes_at_their_ends(M, K):
+    """Scales of 2^-127 and 2^127 that meet in one product, sums below fp32's
+    normal numbers, and NaN scales: every row and column has one scale."""
+    rng = np.random.default_rng(M + K)
+    N = 72
+    sa = rng.choice([0, 1, 2, 60, 127, 128, 190, 250, 253, 255], M).astype(np.uint8)
+    sw = rng.choice([0, 1, 2, 60, 127, 128, 190, 253, 255], N).astype(np.uint8)
+    a = rng.integers(0, 256, (M, K // 2), dtype=np.uint8), np.repeat(sa[:, None], K // 32, axis=1)
+    w = rng.integers(0, 256, (N, K // 2), dtype=np.uint8), np.repeat(sw[:, None], K // 32, axis=1)
+    got = host_bf16_f32(nv.mx_gemm_packed(dev(a[0]), dev(a[1]), dev(w[0]), dev(w[1]))).astype(np.float64)
+    nan = (sa == 255)[:, None] | (sw == 255)[None, :]
+    assert np.isnan(got[nan]).all() and nan.any()
+    A, W = (ref.mx_decode(c, np.full_like(s, 127)) for c, s in (a, w))
+    scale = np.exp2(sa.astype(np.float64)[:, None] + sw.astype(np.float64)[None, :] - 254.0)
+    want, mag = A @ W.T * scale, np.abs(A) @ np.abs(W).T * scale
+    # (sums of whole quarters below 36 K: exact)
+    normal = ~nan & (mag < 2.0 ** 127) & (np.abs(want) >= 2.0 ** -126)
+    assert normal.sum() > 50
+    rounded = ref.bf16_values(ref.bf16_round(np.where(normal, want, 0.0)))
+    assert np.array_equal(got[normal], rounded[normal])
+    # below the normal numbers a sum may flush to 0.  (Where the magnitudes add up
+    # past fp32's range nothing is required: of 2^127 + .. - 2^127 - .. = 0 the
+    # partial sums can be infinite in fp32.)
+    tiny = ~nan & (mag < 2.0 ** 127) & (np.abs(want) < 2.0 ** -126)
+    assert tiny.sum() > 50
+    assert (np.abs(got[tiny]) <= 2.0 ** -126).all()
