@@ -12,9 +12,11 @@
 // pick the experts; every lane of the token sees each winner, and lane j
 // keeps slot j's.
 //
-// Measured on MI355X: 4096 x 256 fp32, top 8, 6.5 us (a launch takes about 2);
-// the dense gradient of 65536 x 256 bf16, 71 MB read and written, 18.5 us,
-// 3.8 TB/s, bound by its exponentials and the passes through LDS.
+// Measured on MI355X: 4096 x 256 fp32, top 8, 6.8 us (a launch takes about 2):
+// each of the rounds scans a lane's keys twice and reduces twice, one after the
+// other.  65536 tokens 34 us, 2.1 TB/s; 4096 x 1024 12.7 us.  The dense gradient
+// of 65536 x 256 bf16, 71 MB read and written, 17.8 us, 4.0 TB/s, bound by its
+// exponentials and the passes through LDS.
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 
@@ -427,8 +429,17 @@ hipError_t gate_dispatch(const nvfp4_gate_config& c, GateArgs a, bool backward, 
     a.E = (int32_t)c.E;
     a.top_k = (int32_t)c.top_k;
     a.scale = c.scale;
-    // (measured with E = 256, top_k 8 on MI355X: see the file's head; the
-    // gradient's row passes want whole waves of tokens at any T)
+    // A whole wave per token / four tokens a wave, us on MI355X, fp32, top_k 8,
+    // softmax and (in brackets) sigmoid with a bias and 8 groups:
+    //   E = 64   1024 tokens 4.1 / 3.7 (7.0 / 6.7), 2048 4.8 / 3.7 (8.1 / 6.7),
+    //     16384 17.3 / 5.9 (34.0 / 11.1)
+    //   128      1024 4.1 / 4.4 (6.9 / 9.1), 2048 4.7 / 4.5 (8.2 / 9.1), 4096 6.7
+    //     / 5.1 (11.9 / 9.9), 16384 17.3 / 7.7 (34.3 / 17.1)
+    //   256      2048 5.0 / 6.8 (8.8 / 15.4), 4096 6.8 / 6.9 (12.3 / 15.5), 16384
+    //     18.1 / 12.1 (36.0 / 29.6)
+    // One border between them, where 128 experts cross; 256 would cross at 4096
+    // (8192 and more with groups).  The gradient's row passes want whole waves of
+    // tokens at any T.
     if (c.E <= 256 && c.top_k <= 16 && (backward || c.T > 2048)) {
         if (c.E <= 64) return gate_types<16, 4>(c, a, backward, s);
         if (c.E <= 128) return gate_types<16, 8>(c, a, backward, s);

@@ -106,16 +106,16 @@ struct MxMoeLayout {
 // can meet on an expert, else sorted by expert, in row tiles of 16 on the
 // streaming kernel or of kMxMoeBM on the LDS tiles.  Measured on MI355X (us,
 // slots / 16 rows / LDS tiles), E experts of H x I, uniform routing:
-//   E = 256, 6144 x 2048, top 8   4 tokens 133 / 136 / 152, 8: 257 / 248 / 268,
-//     64: 1954 / 850 / 847, 128: - / 982 / 971, 512: - / 1424 / 1035
-//   256, 2048 x 1024, top 8       8: 44 / 52 / 77, 16: 88 / 90 / 125,
-//     256: - / 201 / 225, 512: - / 275 / 232
-//   64, 2048 x 1408, top 6        4: 29 / 33 / 57, 8: 47 / 47 / 79,
-//     128: - / 79 / 100, 256: - / 122 / 105
-//   32, 2048 x 1024, top 4        8: 31 / 30 / 52, 128: - / 56 / 61,
-//     256: - / 65 / 62
-//   8, 4096 x 2048, top 2         4: 28 / 33 / 50, 8: 46 / 35 / 68,
-//     64: - / 43 / 56, 128: - / 64 / 56
+//   E = 256, 6144 x 2048, top 8   4 tokens 121 / 140 / 153, 8: 240 / 240 / 266,
+//     64: 1761 / 838 / 842, 128: - / 1009 / 980, 512: - / 1441 / 1040
+//   256, 2048 x 1024, top 8       8: 52 / 59 / 83, 16: 91 / 88 / 121,
+//     256: - / 202 / 223, 512: - / 276 / 233
+//   64, 2048 x 1408, top 6        4: 30 / 36 / 59, 8: 50 / 50 / 84,
+//     128: - / 84 / 105, 256: - / 126 / 108
+//   32, 2048 x 1024, top 4        8: 32 / 29 / 52, 128: - / 49 / 62,
+//     256: - / 68 / 64
+//   8, 4096 x 2048, top 2         4: 28 / 33 / 51, 8: 50 / 36 / 60,
+//     64: - / 47 / 62, 128: - / 66 / 64
 enum class MoePlan { kSlots, kStream, kTiles };
 MoePlan plan_mx_moe(const nvfp4_mx_moe_problem& p) {
     const int64_t S = p.T * p.top_k, expert = p.I * p.H / 2 * 3;  // an expert's codes, in bytes

@@ -27,10 +27,10 @@
 // Blocks past K and rows past the operand load as zeros.
 //
 // Bound by the matrix units' power on large plain products (4096 x 6144 x
-// 16384 on MI355X: 220 us, 3.75 PFLOP/s; the instruction alone keeps 3.8 to 4.0
-// on random codes), by the weights on the routed layer (4096 tokens, 8 of 256
-// experts of 6144 x 2048: 807 us for 3.8 GB and 530 us for 2.6 GB, read and
-// written).
+// 16384 on MI355X: 220 to 230 us, 3.6 to 3.75 PFLOP/s; the instruction alone
+// keeps 3.8 to 4.0 on random codes), by the weights on the routed layer (4096 tokens, 8 of 256
+// experts of 6144 x 2048: 807 to 836 us for 3.8 GB and 530 to 541 us for 2.6 GB,
+// read and written).
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 #include "nvfp4_dma.hpp"
@@ -529,9 +529,9 @@ __global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part,
 }  // namespace
 
 // K splits of the 128 x 128 tiles: while the tiles leave CUs without one and
-// every split keeps eight K steps (64 rows x 6144 x 16384 in 10 splits: 22 us;
-// 256 rows x 16384 x 2048, 256 tiles of 8 steps, in two: 25 us against 15
-// unsplit).
+// every split keeps eight K steps (64 rows x 6144 x 16384 in 8 splits: 25 us;
+// 256 rows x 16384 x 2048, 256 tiles of 8 steps, in two: 26 us against 14
+// unsplit; weights from memory).
 int mx_gemm_splits(int64_t M, int64_t N, int64_t K, int* steps) {
     const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), ksteps = (K + 255) / 256;
     int64_t s = std::min<int64_t>({512 / std::max<int64_t>(tiles, 1), ksteps / 8, 16});

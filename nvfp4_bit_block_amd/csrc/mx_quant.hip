@@ -176,6 +176,8 @@ bool mx_quantize_cols_fits(int64_t rows, int64_t cols) {
 
 // 256-row tiles write whole cache lines of codes; below two of them per CU,
 // 32-row tiles give eight times the workgroups (1056 x 1021: 11.0 -> 4.9 us).
+// 4096 x 6144 takes 14.3 us, 4.5 TB/s (along rows 12.5), 65536 x 6144 246 us, 4.2
+// TB/s (155): a lane reads its column from LDS two bytes at a time.
 hipError_t launch_mx_quantize_cols(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes_t, uint8_t* scales_t,
                                    hipStream_t stream) {
     const int64_t rt = (rows + 255) / 256, ct = (cols + 63) / 64;

@@ -1,10 +1,13 @@
 // mx_stream.hip -- MXFP4 products for few activation rows: every weight byte
 // is read once, straight from memory into the matrix instruction's operand
 // registers, and nothing else is large.  Bound by the weight stream, and by a
-// launch's ramp and tail where that is short: on MI355X one token through 6144
-// x 16384 takes 10.9 us (53.5 MB, 4.9 TB/s), the gate/up product of its 8
-// experts of 6144 x 2048 23.8 us (107 MB, 4.5 TB/s) and the down product 11.9
-// us (53.5 MB, 4.5 TB/s).
+// launch's ramp and tail where that is short.  On MI355X, kernel times over
+// eight sets of weights in turn, so that they come from memory: one token
+// through 6144 x 16384 13.0 us (53.5 MB, 4.1 TB/s; 10.4 while three sets stay in
+// the last-level cache), the gate/up product of its 8 experts of 6144 x 2048
+// 24.1 us (107 MB, 4.4 TB/s) and the down product 12.0 us (53.5 MB, 4.5 TB/s).
+// The figures below are times per call in a graph, weights of 0.4 GB or more in
+// turn where one set is larger than 16 MB.
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4, weights as the A operand (16 weight
 // rows), activations as the B operand (16 rows, fewer are padded with copies
@@ -39,8 +42,9 @@ namespace {
 // more than 128 registers, so that several workgroups share a CU (one loads
 // while another adds up).
 constexpr int waves_of(int nr) { return nr == 4 ? 4 : 8; }
-// Waves per SIMD: four, or three where a wave has four tiles (64 tokens, 8 of
-// 256 experts, 6144 x 2048: 814 us, where two take 853 and four 888).
+// Waves per SIMD: four, or three where a wave has four tiles, between what the
+// large layers and the small ones like best (two / three / four; 64 tokens, 8 of
+// 256 experts, 6144 x 2048: 823 / 840 / 889 us, 2048 x 1024: 162 / 163 / 157).
 constexpr int wpe_of(int nr, int mb) { return nr * mb <= 2 ? 4 : 3; }
 
 // One operand: uniform bases of codes and scales and the bytes that are
@@ -79,8 +83,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint3
 // buffer, so that the range check holds whichever way it counts it.)  Loads
 // that keep their lines, not non-temporal ones: an instruction reads half a
 // cache line of each row and the next one the other half, which a line that is
-// not kept fetches again (28.1 against 18.9 us for one token's gate/up product
-// of 8 experts, 6144 x 2048).
+// not kept fetches again (one token's layer of 8 experts, 6144 x 2048: 41.0
+// against 36.4 us; 64 tokens, 8 of 256: 1092 against 868).
 template <int USTEPS>
 __device__ __forceinline__ Unit<USTEPS> load_unit(const Rows& r, const RowAt& at, int unit, bool live, int g, int nblk) {
     Unit<USTEPS> u;
@@ -168,8 +172,8 @@ struct SliceItem {
 
 // The same for packed rows, which are only copied: a lane then loads its piece
 // of the activation once, where the operand's layout has every 16 lanes load a
-// row again with each unit of weights (one packed row through 6144 x 16384 16.0
-// -> 12.9 us, the down product of a token's 8 experts 14.8 -> 11.9).
+// row again with each unit of weights (one packed row through 6144 x 16384 15.8
+// -> 12.5 us, four 16.4 -> 14.3, a token's layer of 8 experts 39.1 -> 36.4).
 struct PackedItem {
     u32x4 c;
     uint32_t s;
@@ -481,8 +485,8 @@ int slice_of(int64_t K, int usteps, int waves) {
 // Weight rows of a tile: 16, or 12 or 8 where that spreads the tiles more
 // evenly over the 256 CUs (6144 rows: 384 tiles of 16 leave half the CUs with
 // two and half with one; 512 of 12 give each two: one token through 6144 x
-// 16384 12.9 -> 11.5 us, through the down projection of 8 experts 6144 x 2048
-// 14.5 -> 12.6 us).  With more than 16 activation rows a workgroup's reads of
+// 16384 14.4 -> 13.2 us, packed 13.5 -> 12.5, through 8 experts of 6144 x 2048
+// 38.5 -> 36.4).  With more than 16 activation rows a workgroup's reads of
 // them count, and fewer, whole tiles win (37 x 4099 x 2080: 6.0 against 7.1).
 int rows_per_tile(int64_t N, int nr) {
     auto most = [&](int64_t rt) { return ((N + rt * nr - 1) / (rt * nr) + 255) / 256 * rt; };  // rows of the fullest CU
@@ -538,8 +542,9 @@ hipError_t launch_k(const MxStreamArgs& g, int64_t mtiles, hipStream_t stream) {
 
 }  // namespace
 
-// Every workgroup quantizes the rows for itself: 2 us for one row of 16384,
-// 7.5 us for four, against about 4 us for a launch of its own.  (LDS: the
+// Every workgroup quantizes the rows for itself: through 6144 x 16384 two rows
+// take 15.9 us that way (14.3 for four packed ones), three 17.4 against 16.7
+// with a launch of its own, four 18.7 against 17.4.  (LDS: the
 // largest of the forms, four waves, units of up to four steps.)
 static bool fits_lds(int64_t M, int64_t K) {
     return K <= ((int64_t)1 << 20) && M * (K / 32 + 16 * 8) * 17 <= 64 * 1024;
@@ -558,9 +563,11 @@ static int plain_tiles(int64_t M, int64_t N, int64_t K) {
 }
 
 // Every workgroup reads the activation, so with more rows that becomes the
-// larger stream: at 6144 x 16384 4 rows take 14.5 us, 8 18.6, 16 22 and 64 57,
-// where the LDS tiles take 17 for up to 16 and 21 for 64; 32 rows of 16384 x
-// 2048 take 10 us either way.
+// larger stream.  Streaming against the LDS tiles, us: 6144 x 16384 4 rows 13.7
+// / 20.8, 8 16.9 / 21.0, 16 19.9 / 21.1, 32 35.6 / 22.3, 64 58.0 / 25.0; 16384 x
+// 2048 16 rows 7.1 / 12.1, 32 9.6 / 12.4, 64 20.9 / 12.6.  (The border was set
+// with the weights in the last-level cache, where the tiles take 17 at 6144 x
+// 16384: from memory 8 and 16 rows of it lie on the wrong side, by 4 and 1 us.)
 bool mx_stream_takes(int64_t M, int64_t N, int64_t K) {
     if (M > 64) return false;
     if (M <= 4) return true;
