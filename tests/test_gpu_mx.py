@@ -4,9 +4,10 @@ the 64-bit definition (tests/mx_reference.py).
 Quantize and dequantize: bit for bit.  Products: the codes' products are exact
 and are summed in fp32 in some order, so the sum is off by at most
 K * 2^-23 of the sum of magnitudes (2^-23 rather than a half step: the matrix
-units may truncate), then one rounding to bf16, 2^-8 relative.  The layer
-rounds each slot's result to bf16 when it sorts the slots by expert (at most
-2^-8 of the slot's result, so 2^-8 of the sum of their magnitudes) and
+units may truncate), then one rounding to bf16, 2^-8 relative.  The layer's
+bound here leaves room for a rounding of each slot's result to bf16 (2^-8 of
+the sum of their magnitudes), which the layer does not make
+(tests/test_gpu_mx_experts.py bounds it without), and
 adds the rounding of h to bf16 and to MXFP4, which the definition has too: an
 h that lies closer to a border than the error of its sum may take the
 neighbouring code, so the layer's inputs here give sums that fp32 holds
@@ -299,7 +300,7 @@ def test_experts_past_32_bits():
     w2 = (torch.empty((E, H, I // 2), dtype=torch.uint8, device=d), r(118, 122, E, H, I // 32))
     assert (E - 1) * w13[0][0].numel() > 2 ** 31
     w13[0][-1], w2[0][-1] = r(0, 256, 2 * I, H // 2), r(0, 256, H, I // 2)
-    for T in (2, 40, 4000):                                            # slots, streamed rows, tiles
+    for T in (2, 40, 4000):                                            # slots, slots, tiles
         x = torch.randn((T, H), generator=g, device=d).to(torch.bfloat16)
         ids = torch.full((T, 1), E - 1, dtype=torch.int32, device=d)
         tw = torch.ones((T, 1), device=d)
